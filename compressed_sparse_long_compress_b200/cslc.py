@@ -31,6 +31,8 @@ ABI_SYMBOLS = [
     "csa_compress_front_end", "hca_compress_front_end",
     "csa_indexer_topk_bf16_workspace_bytes", "csa_indexer_topk_bf16", "csa_topk_bf16",
     "cslc_testing_set_wait_limits", "cslc_quantize_rows_e4m3", "csa_indexer_topk_fp8",
+    "cslc_page_plan", "cslc_page_write_e4m3", "cslc_prompt_attn_workspace_bytes", "cslc_prompt_attn",
+    "cslc_page_decode_workspace_bytes", "cslc_page_decode_attn",
 ]
 
 
@@ -85,6 +87,15 @@ def _load():
         "csa_indexer_topk_fp8": (c_int, [P, P, P, P, P, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                                          P, P, P, c_size_t, P]),
         "hca_compress_front_end": (c_int, [P, P, P, c_int, c_int, c_int, c_int, P, P]),
+        "cslc_page_plan": (c_int, [P, P, c_int, P, c_int, c_int, c_int, c_int, c_int, P, P, P, P, P, P]),
+        "cslc_page_write_e4m3": (c_int, [P, P, P, c_int, c_int, c_int, c_int, c_int, ctypes.c_int64, ctypes.c_int64,
+                                         P, P, P, P, P]),
+        "cslc_prompt_attn_workspace_bytes": (c_size_t, [c_int, c_int, c_int, c_int]),
+        "cslc_prompt_attn": (c_int, [P, P, P, P, P, c_int, c_int, c_int, c_int, c_int, c_int, ctypes.c_int64,
+                                     ctypes.c_int64, ctypes.c_int64, c_int, c_float, P, P, P, c_size_t, P]),
+        "cslc_page_decode_workspace_bytes": (c_size_t, [c_int, c_int, c_int]),
+        "cslc_page_decode_attn": (c_int, [P, P, P, P, P, P, P, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                                          ctypes.c_int64, c_int, c_float, P, P, P, c_size_t, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -461,3 +472,160 @@ def decode_append(state: AppendState, c, z, pos, pos_bias, nope, rope, kv_scale,
                                   B, state.m, int(state.overlap), _ptr(state.ring_c), _ptr(state.ring_z),
                                   _ptr(state.ring_kc), _ptr(state.ring_kz), _ptr(nope), _ptr(rope), _ptr(kv_scale),
                                   _ptr(k_idx), n_max, _ptr(n_entries), _stream(stream)))
+
+
+# ------------------------------------------- uncompressed attention, paged cache
+
+def _rows(t, dtype, name, device, shape):
+    """As _need for rows of heads [rows, heads, 128] that may lie apart: dense
+    within a row, any row stride that is a multiple of 8 elements. Returns the stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, expected a CUDA device, {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    n, h, d = shape
+    if h * d and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name} must be dense within a row")
+    return t.stride(0) if n > 1 else h * d
+
+
+def _at(t, dtype, name, device, shape=None):
+    """As _need, on the given device."""
+    _need(t, dtype, name, shape)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t
+
+
+def _alloc(shape, dtype, device, stream):
+    """Memory for a call on `stream`: from that stream's pool, so that it is not
+    reused by another stream's work while the call still runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _run_on(device, stream, fn, *args):
+    """fn(*args, stream) with the tensors' device current."""
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    if s.device != device:
+        raise ValueError(f"the stream is on {s.device}, the tensors on {device}")
+    with torch.cuda.device(device):
+        _check(fn(*args, ctypes.c_void_p(s.cuda_stream)))
+
+
+def page_plan(old_len, new_len, free_pages, block_table, page: int, n_pages: int, max_tokens: int | None = None,
+              slots=None, cu=None, seq_len=None, status=None, stream=None):
+    """Hands out pages to requests of old_len [B] tokens that get new_len [B] more
+    and lists the new tokens' slots (see cslc_page_plan in include/cslc.h).
+    block_table [B, max_pages] is updated in place. Pass max_tokens (the most new
+    tokens of a step) or slots [max_tokens]. Returns (slots, cu [B + 1], seq_len
+    [B], status [2]: pages handed out, tokens without a page)."""
+    dev = block_table.device
+    B, max_pages = block_table.shape
+    _at(old_len, I32, "old_len", dev, (B,)); _at(new_len, I32, "new_len", dev, (B,))
+    _at(free_pages, I32, "free_pages", dev, (free_pages.numel(),)); _at(block_table, I32, "block_table", dev)
+    if slots is None:
+        if max_tokens is None:
+            raise ValueError("page_plan: give max_tokens or slots")
+        slots = _alloc((max_tokens,), I32, dev, stream)
+    cu = _alloc((B + 1,), I32, dev, stream) if cu is None else cu
+    seq_len = _alloc((B,), I32, dev, stream) if seq_len is None else seq_len
+    status = _alloc((2,), I32, dev, stream) if status is None else status
+    _at(slots, I32, "slots", dev, (slots.numel(),)); _at(cu, I32, "cu", dev, (B + 1,))
+    _at(seq_len, I32, "seq_len", dev, (B,)); _at(status, I32, "status", dev, (2,))
+    _run_on(dev, stream, LIB.cslc_page_plan, _ptr(old_len), _ptr(new_len), B, _ptr(free_pages), free_pages.numel(), page,
+            n_pages, max_pages, slots.numel(), _ptr(block_table), _ptr(slots), _ptr(cu), _ptr(seq_len), _ptr(status))
+    return slots, cu, seq_len, status
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, device):
+    n_pages, Hkv, P, D = k_cache.shape
+    _at(k_cache, U8, "k_cache", device); _at(v_cache, U8, "v_cache", device, k_cache.shape)
+    _at(k_scale, F32, "k_scale", device, (n_pages, Hkv)); _at(v_scale, F32, "v_scale", device, (n_pages, Hkv))
+    return n_pages, Hkv, P, D
+
+
+def page_write_e4m3(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
+    """Quantises k, v [T, H_kv, 128] bf16 (rows may lie apart) into their slots [T]
+    of the paged cache, in place: caches [n_pages, H_kv, P, 128] uint8 e4m3 codes,
+    scales [n_pages, H_kv] fp32 (see cslc_page_write_e4m3 in include/cslc.h)."""
+    dev = k_cache.device
+    n_pages, Hkv, P, D = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    T = slots.numel()
+    ks = _rows(k, BF16, "k", dev, (T, Hkv, D)); vs = _rows(v, BF16, "v", dev, (T, Hkv, D))
+    _at(slots, I32, "slots", dev, (T,))
+    _run_on(dev, stream, LIB.cslc_page_write_e4m3, _ptr(k), _ptr(v), _ptr(slots), T, Hkv, D, P, n_pages, ks, vs,
+            _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale))
+
+
+def prompt_attn_workspace_bytes(B: int, Tq: int, H: int, Hkv: int) -> int:
+    return LIB.cslc_prompt_attn_workspace_bytes(B, Tq, H, Hkv)
+
+
+def prompt_attn(q, k, v, cu_q, cu_k, scale: float, window: int = 0, out=None, lse=None, ws=None, stream=None):
+    """Causal attention of packed sequences with grouped heads: q [Tq, H, 128],
+    k, v [Tk, H_kv, 128] bf16 (rows may lie apart), cu_q, cu_k [B + 1] int32 (see
+    cslc_prompt_attn in include/cslc.h). Rows of no sequence are left as they
+    were. lse=True allocates it. Returns (out [Tq, H, 128], lse [Tq, H] or None)."""
+    dev = q.device
+    Tq, H, D = q.shape
+    Tk, Hkv = k.shape[:2]
+    B = cu_q.numel() - 1
+    qs = _rows(q, BF16, "q", dev, (Tq, H, D))
+    ks = _rows(k, BF16, "k", dev, (Tk, Hkv, D)); vs = _rows(v, BF16, "v", dev, (Tk, Hkv, D))
+    if B < 0:
+        raise ValueError("cu_q must have B + 1 entries")
+    _at(cu_q, I32, "cu_q", dev, (B + 1,)); _at(cu_k, I32, "cu_k", dev, (B + 1,))
+    out = _alloc((Tq, H, D), BF16, dev, stream) if out is None else _at(out, BF16, "out", dev, (Tq, H, D))
+    if lse is True:
+        lse = _alloc((Tq, H), F32, dev, stream)
+    if lse is not None:
+        _at(lse, F32, "lse", dev, (Tq, H))
+    nbytes = LIB.cslc_prompt_attn_workspace_bytes(B, Tq, H, Hkv)
+    if ws is None and nbytes:
+        ws = _alloc((nbytes,), U8, dev, stream)
+    if ws is not None:
+        _at(ws, U8, "ws", dev)
+    _run_on(dev, stream, LIB.cslc_prompt_attn, _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, H, Hkv, D,
+            qs, ks, vs, window, float(scale), _ptr(out), _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel())
+    return out, lse
+
+
+def page_decode_workspace_bytes(B: int, H: int, Hkv: int) -> int:
+    return LIB.cslc_page_decode_workspace_bytes(B, H, Hkv)
+
+
+def page_decode_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len, scale: float, window: int = 0,
+                     out=None, lse=None, ws=None, stream=None):
+    """Attention of one new token per sequence, q [B, H, 128] bf16 (rows may lie
+    apart), over the paged e4m3 cache (see cslc_page_decode_attn in
+    include/cslc.h). lse=True allocates it. Returns (out [B, H, 128], lse [B, H]
+    or None)."""
+    dev = q.device
+    B, H, D = q.shape
+    n_pages, Hkv, P, Dc = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    if Dc != D:
+        raise ValueError(f"the cache holds rows of {Dc}, q of {D}")
+    qs = _rows(q, BF16, "q", dev, (B, H, D))
+    max_pages = block_table.shape[1]
+    _at(block_table, I32, "block_table", dev, (B, max_pages)); _at(seq_len, I32, "seq_len", dev, (B,))
+    out = _alloc((B, H, D), BF16, dev, stream) if out is None else _at(out, BF16, "out", dev, (B, H, D))
+    if lse is True:
+        lse = _alloc((B, H), F32, dev, stream)
+    if lse is not None:
+        _at(lse, F32, "lse", dev, (B, H))
+    nbytes = LIB.cslc_page_decode_workspace_bytes(B, H, Hkv)
+    if ws is None and nbytes:
+        ws = _alloc((nbytes,), U8, dev, stream)
+    if ws is not None:
+        _at(ws, U8, "ws", dev)
+    _run_on(dev, stream, LIB.cslc_page_decode_attn, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            _ptr(block_table), _ptr(seq_len), B, H, Hkv, D, P, n_pages, max_pages, qs, window, float(scale), _ptr(out),
+            _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel())
+    return out, lse

@@ -57,7 +57,21 @@ size_t decode_topk_workspace_bytes(int, int, int);
 cslc_status run_decode_step(const cslc_decode_layer*, int, int, int, int, void*, size_t, cudaStream_t);
 cslc_status run_decode_topk(const float*, const int32_t*, int, int, int, int32_t*, void*, cudaStream_t);
 
+cslc_status launch_page_plan(const int32_t*, const int32_t*, int, const int32_t*, int, int, int, int, int, int32_t*,
+                             int32_t*, int32_t*, int32_t*, int32_t*, cudaStream_t);
+cslc_status launch_page_write(const uint16_t*, const uint16_t*, const int32_t*, int, int, int, int, long long,
+                              long long, uint8_t*, uint8_t*, float*, float*, cudaStream_t);
+size_t prompt_attn_workspace_bytes(int, int, int, int);
+cslc_status launch_prompt_attn(const uint16_t*, const uint16_t*, const uint16_t*, const int32_t*, const int32_t*, int,
+                               int, int, int, int, long long, long long, long long, int, float, uint16_t*, float*,
+                               void*, cudaStream_t);
+size_t page_decode_workspace_bytes(int, int, int);
+cslc_status launch_page_decode(const uint16_t*, const uint8_t*, const uint8_t*, const float*, const float*,
+                               const int32_t*, const int32_t*, int, int, int, int, int, int, long long, int, float,
+                               uint16_t*, float*, void*, cudaStream_t);
+
 constexpr int kMaxTopk = 2048;
+constexpr int kMaxSeqs = 8192;              // sequences of one call of the paged entry points
 constexpr int kMaxPrefillTopkNc = 786432;   // a row's selection masks (Nc / 4 bytes) fit in shared memory
 
 static bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
@@ -489,6 +503,129 @@ cslc_status cslc_decode_topk(const float* scores, const int32_t* n_entries, int 
           "cslc_decode_topk: workspace of %zu bytes needed", need);
   REQUIRE(aligned16(ws), CSLC_ERR_ALIGN, "cslc_decode_topk: ws is not 16-byte aligned");
   return run_decode_topk(scores, n_entries, B, n_max, topk, idx, ws, stream);
+}
+
+// --------------------------------------------------- uncompressed attention, paged cache
+
+static cslc_status check_pages(const char* fn, int Hkv, int page, int n_pages) {
+  REQUIRE(page == 16 || page == 32 || page == 64 || page == 128, CSLC_ERR_UNSUPPORTED,
+          "%s: the page size must be 16, 32, 64 or 128 (got %d)", fn, page);
+  REQUIRE(n_pages >= 0, CSLC_ERR_SHAPE, "%s: negative size", fn);
+  REQUIRE((long long)n_pages * Hkv * page < (1ll << 31), CSLC_ERR_UNSUPPORTED,
+          "%s: n_pages * H_kv * page must be below 2^31", fn);
+  return CSLC_OK;
+}
+
+static cslc_status check_heads(const char* fn, int H, int Hkv, int D) {
+  REQUIRE(D == kD, CSLC_ERR_UNSUPPORTED, "%s: D must be 128 (got %d)", fn, D);
+  REQUIRE(H >= 1 && H <= 128 && Hkv >= 1 && H % Hkv == 0, CSLC_ERR_UNSUPPORTED,
+          "%s: H must be in [1, 128] and a multiple of H_kv", fn);
+  return CSLC_OK;
+}
+
+static cslc_status check_stride(const char* fn, const char* what, long long stride, int heads) {
+  REQUIRE(stride >= (long long)heads * kD && stride % 8 == 0 && stride < (1ll << 36), CSLC_ERR_UNSUPPORTED,
+          "%s: %s must be a multiple of 8, at least %d and below 2^36", fn, what, heads * kD);
+  return CSLC_OK;
+}
+
+#define FORWARD(call)                          \
+  do {                                         \
+    const cslc_status st_ = (call);            \
+    if (st_ != CSLC_OK) return st_;            \
+  } while (0)
+
+cslc_status cslc_page_plan(const int32_t* old_len, const int32_t* new_len, int B, const int32_t* free_pages,
+                           int n_free, int page, int n_pages, int max_pages, int max_tokens, int32_t* block_table,
+                           int32_t* slots, int32_t* cu, int32_t* seq_len, int32_t* status, cslc_stream_t stream) {
+  REQUIRE(B >= 0 && n_free >= 0 && max_pages >= 0 && max_tokens >= 0, CSLC_ERR_SHAPE, "cslc_page_plan: negative size");
+  REQUIRE(B <= kMaxSeqs, CSLC_ERR_UNSUPPORTED, "cslc_page_plan: at most %d sequences", kMaxSeqs);
+  FORWARD(check_pages("cslc_page_plan", 1, page, n_pages));
+  REQUIRE_PTR(cu); REQUIRE_PTR(status);
+  if (B > 0) {
+    REQUIRE_PTR(old_len); REQUIRE_PTR(new_len); REQUIRE_PTR(seq_len);
+    if (max_pages > 0) REQUIRE_PTR(block_table);
+  }
+  if (n_free > 0) REQUIRE_PTR(free_pages);
+  if (max_tokens > 0) REQUIRE_PTR(slots);
+  return launch_page_plan(old_len, new_len, B, free_pages, n_free, page, n_pages, max_pages, max_tokens, block_table,
+                          slots, cu, seq_len, status, stream);
+}
+
+cslc_status cslc_page_write_e4m3(const cslc_bf16* k, const cslc_bf16* v, const int32_t* slots, int T, int Hkv, int D,
+                                 int page, int n_pages, int64_t k_stride, int64_t v_stride, uint8_t* k_cache,
+                                 uint8_t* v_cache, float* k_scale, float* v_scale, cslc_stream_t stream) {
+  const char* fn = "cslc_page_write_e4m3";
+  REQUIRE(T >= 0, CSLC_ERR_SHAPE, "%s: negative size", fn);
+  FORWARD(check_heads(fn, Hkv, Hkv, D));
+  FORWARD(check_pages(fn, Hkv, page, n_pages));
+  FORWARD(check_stride(fn, "k_stride", k_stride, Hkv));
+  FORWARD(check_stride(fn, "v_stride", v_stride, Hkv));
+  REQUIRE((long long)T * 2 * Hkv < (1ll << 31), CSLC_ERR_UNSUPPORTED, "%s: T * 2 * H_kv must be below 2^31", fn);
+  if (T == 0 || n_pages == 0) return CSLC_OK;
+  REQUIRE_PTR(k); REQUIRE_PTR(v); REQUIRE_PTR(slots);
+  REQUIRE_PTR(k_cache); REQUIRE_PTR(v_cache); REQUIRE_PTR(k_scale); REQUIRE_PTR(v_scale);
+  return launch_page_write(k, v, slots, T, Hkv, page, n_pages, k_stride, v_stride, k_cache, v_cache, k_scale, v_scale,
+                           stream);
+}
+
+size_t cslc_prompt_attn_workspace_bytes(int B, int Tq, int H, int Hkv) {
+  if (B <= 0 || Tq <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0) return 0;
+  return prompt_attn_workspace_bytes(B, Tq, H, Hkv);
+}
+
+cslc_status cslc_prompt_attn(const cslc_bf16* q, const cslc_bf16* k, const cslc_bf16* v, const int32_t* cu_q,
+                             const int32_t* cu_k, int B, int Tq, int Tk, int H, int Hkv, int D, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, int window, float scale, cslc_bf16* out, float* lse,
+                             void* ws, size_t ws_bytes, cslc_stream_t stream) {
+  const char* fn = "cslc_prompt_attn";
+  REQUIRE(B >= 0 && Tq >= 0 && Tk >= 0 && window >= 0, CSLC_ERR_SHAPE, "%s: negative size", fn);
+  REQUIRE(B <= kMaxSeqs, CSLC_ERR_UNSUPPORTED, "%s: at most %d sequences", fn, kMaxSeqs);
+  FORWARD(check_heads(fn, H, Hkv, D));
+  FORWARD(check_stride(fn, "q_stride", q_stride, H));
+  FORWARD(check_stride(fn, "k_stride", k_stride, Hkv));
+  FORWARD(check_stride(fn, "v_stride", v_stride, Hkv));
+  REQUIRE((long long)Tq * H < (1ll << 31) && (long long)Tk * Hkv < (1ll << 31), CSLC_ERR_UNSUPPORTED,
+          "%s: Tq * H and Tk * H_kv must be below 2^31", fn);
+  if (B == 0 || Tq == 0) return CSLC_OK;
+  REQUIRE_PTR(q); REQUIRE_PTR(cu_q); REQUIRE_PTR(cu_k); REQUIRE_PTR(out);
+  if (Tk > 0) { REQUIRE_PTR(k); REQUIRE_PTR(v); }
+  if (lse) REQUIRE_PTR(lse);
+  const size_t need = prompt_attn_workspace_bytes(B, Tq, H, Hkv);
+  REQUIRE(need == 0 || (ws != nullptr && ws_bytes >= need), CSLC_ERR_WORKSPACE, "%s: workspace of %zu bytes needed",
+          fn, need);
+  REQUIRE(aligned16(ws), CSLC_ERR_ALIGN, "%s: ws is not 16-byte aligned", fn);
+  return launch_prompt_attn(q, k, v, cu_q, cu_k, B, Tq, Tk, H, Hkv, q_stride, k_stride, v_stride, window, scale, out,
+                            lse, ws, stream);
+}
+
+size_t cslc_page_decode_workspace_bytes(int B, int H, int Hkv) {
+  if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0) return 0;
+  return page_decode_workspace_bytes(B, H, Hkv);
+}
+
+cslc_status cslc_page_decode_attn(const cslc_bf16* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                  const float* k_scale, const float* v_scale, const int32_t* block_table,
+                                  const int32_t* seq_len, int B, int H, int Hkv, int D, int page, int n_pages,
+                                  int max_pages, int64_t q_stride, int window, float scale, cslc_bf16* out, float* lse,
+                                  void* ws, size_t ws_bytes, cslc_stream_t stream) {
+  const char* fn = "cslc_page_decode_attn";
+  REQUIRE(B >= 0 && max_pages >= 0 && window >= 0, CSLC_ERR_SHAPE, "%s: negative size", fn);
+  REQUIRE(B <= kMaxSeqs, CSLC_ERR_UNSUPPORTED, "%s: at most %d sequences", fn, kMaxSeqs);
+  FORWARD(check_heads(fn, H, Hkv, D));
+  FORWARD(check_pages(fn, Hkv, page, n_pages));
+  FORWARD(check_stride(fn, "q_stride", q_stride, H));
+  if (B == 0) return CSLC_OK;
+  REQUIRE_PTR(q); REQUIRE_PTR(seq_len); REQUIRE_PTR(out);
+  if (max_pages > 0) REQUIRE_PTR(block_table);
+  if (n_pages > 0) { REQUIRE_PTR(k_cache); REQUIRE_PTR(v_cache); REQUIRE_PTR(k_scale); REQUIRE_PTR(v_scale); }
+  if (lse) REQUIRE_PTR(lse);
+  const size_t need = page_decode_workspace_bytes(B, H, Hkv);
+  REQUIRE(need == 0 || (ws != nullptr && ws_bytes >= need), CSLC_ERR_WORKSPACE, "%s: workspace of %zu bytes needed",
+          fn, need);
+  REQUIRE(aligned16(ws), CSLC_ERR_ALIGN, "%s: ws is not 16-byte aligned", fn);
+  return launch_page_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len, B, H, Hkv, page, n_pages,
+                            max_pages, q_stride, window, scale, out, lse, ws, stream);
 }
 
 }  // extern "C"

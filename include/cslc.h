@@ -359,6 +359,127 @@ cslc_status cslc_decode_topk(const float* scores, const int32_t* n_entries, int 
                              cslc_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Uncompressed attention layers over a paged 8-bit cache
+ *
+ * The hybrid stack also has layers that attend to the tokens themselves
+ * (first page §1.3: the first layers are sliding-window attention). These four
+ * entry points serve such layers for requests of different lengths: the page
+ * plan, the cache write, the attention of whole prompts and the attention of
+ * single new tokens.
+ *
+ * The cache holds pages of P tokens (P = 16, 32, 64 or 128), for keys and for
+ * values:
+ *   codes  [n_pages, H_kv, P, 128] uint8 (e4m3)
+ *   scale  [n_pages, H_kv] fp32, a power of two 2^e with -40 <= e <= 60; a
+ *          stored value is e4m3(code) * scale (exact in bf16)
+ * A slot is page * P + offset. Sequence b's token x lies in page
+ * block_table[b, x / P] at offset x mod P; an entry of block_table outside
+ * [0, n_pages) means that there is no such page. n_pages * P and
+ * n_pages * H_kv * P must be below 2^31.
+ *
+ * Query head h reads key / value head h / (H / H_kv): H is a multiple of H_kv,
+ * 1 <= H <= 128. D must be 128.
+ */
+
+/* Page plan: for requests that hold old_len[b] tokens and get new_len[b] more
+ * (negative lengths count as 0), hands out pages and lists every new token's
+ * slot.
+ *
+ *   old_len, new_len [B] int32; free_pages [n_free] int32: pages that nobody holds
+ *   block_table [B, max_pages] int32, in and out: entries below ceil(old/P) are
+ *       read and kept; entries ceil(old/P) .. min(ceil((old+new)/P), max_pages)-1
+ *       get pages of free_pages, front to back in the order of the sequences
+ *       (-1 once the list is used up); later entries are left as they were
+ *   slots [max_tokens] int32: token i of request b (position old_len[b] + i) is
+ *       packed token cu[b] + i; slots[] holds its slot, or -1 when it has no
+ *       page. Entries from cu[B] on are -1, so that a captured step of
+ *       max_tokens rows can be replayed with fewer tokens
+ *   cu [B + 1] int32: exclusive prefix sums of new_len, cu[B] their sum (tokens
+ *       from max_tokens on have no entry in slots)
+ *   seq_len [B] int32: old_len + new_len
+ *   status [2] int32: pages handed out (more than n_free when the list was too
+ *       short), and new tokens that have no page (0 when all went well)
+ * 0 <= B <= 8192. The caller takes the first status[0] pages off its list.
+ * One launch; no workspace. */
+cslc_status cslc_page_plan(const int32_t* old_len, const int32_t* new_len, int B, const int32_t* free_pages,
+                           int n_free, int page, int n_pages, int max_pages, int max_tokens,
+                           int32_t* block_table, int32_t* slots, int32_t* cu, int32_t* seq_len,
+                           int32_t* status, cslc_stream_t stream);
+
+/* Cache write: quantises the keys and values of T tokens into their slots.
+ *
+ * A run is a stretch of consecutive tokens with consecutive slots of one page
+ * (cslc_page_plan makes one run of each page that a request's new tokens
+ * touch). For each run and head, separately for keys and values:
+ *   e = the smallest exponent with amax <= 448 * 2^e, amax over the run's
+ *       finite |x|, held to [-40, 60];
+ *   a run that begins inside its page (offset > 0) keeps the tokens before it:
+ *       e = max(e, exponent of the page's scale), and where that grows the
+ *       page's scale, the codes before the run move to the new scale (rounded
+ *       to nearest even, exact unless they become subnormal);
+ *   codes = e4m3(x * 2^-e), round to nearest even; values beyond +-448 * 2^e,
+ *       infinities among them, saturate and NaN stays NaN; scale = 2^e.
+ * Codes behind a run's last token are left as they were. Tokens whose slot is
+ * outside [0, n_pages * P) are skipped. One call may hold one run for each
+ * page; where two runs share a page, that page's content is unspecified.
+ *
+ *   k, v [T, H_kv, 128] bf16 with k_stride / v_stride elements from one token
+ *       to the next (multiples of 8, at least H_kv * 128)
+ *   slots [T] int32; caches and scales as above, updated in place
+ * 1 <= H_kv <= 128. One launch; no workspace. */
+cslc_status cslc_page_write_e4m3(const cslc_bf16* k, const cslc_bf16* v, const int32_t* slots, int T, int Hkv, int D,
+                                 int page, int n_pages, int64_t k_stride, int64_t v_stride, uint8_t* k_cache,
+                                 uint8_t* v_cache, float* k_scale, float* v_scale, cslc_stream_t stream);
+
+/* Attention over whole prompts: causal, grouped heads, packed sequences.
+ *
+ * Sequence b has the queries cu_q[b] .. cu_q[b+1]-1 and the keys
+ * cu_k[b] .. cu_k[b+1]-1; its last query sees its last key (with nq queries
+ * and nk keys, query i sees the keys j <= i + nk - nq). With window > 0 it
+ * sees only the last `window` of those.
+ *   o[t,h,:] = sum_j softmax_j(scale * q[t,h,:] . k[j,h',:]) v[j,h',:]
+ * fp32 statistics and accumulation, probabilities rounded to bf16 for their
+ * product with v, bf16 output. A query without a visible key outputs 0 and
+ * lse = -inf. Keys and values that a query does not see have no influence on
+ * it, whatever they hold. Rows of out and lse that belong to no sequence are
+ * left as they were.
+ *
+ *   q [Tq, H, 128], k, v [Tk, H_kv, 128] bf16, with q_stride / k_stride /
+ *       v_stride elements from one token to the next (multiples of 8, at least
+ *       the row's length)
+ *   cu_q, cu_k [B + 1] int32, ascending (limited to [0, Tq] and [0, Tk])
+ *   out [Tq, H, 128] bf16; lse [Tq, H] fp32 (natural log-sum-exp), or NULL
+ *   ws  workspace of cslc_prompt_attn_workspace_bytes() bytes; it belongs to
+ *       one call at a time (also in captured graphs)
+ * 0 <= B <= 8192, window >= 0. */
+size_t cslc_prompt_attn_workspace_bytes(int B, int Tq, int H, int Hkv);
+cslc_status cslc_prompt_attn(const cslc_bf16* q, const cslc_bf16* k, const cslc_bf16* v, const int32_t* cu_q,
+                             const int32_t* cu_k, int B, int Tq, int Tk, int H, int Hkv, int D, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, int window, float scale, cslc_bf16* out, float* lse,
+                             void* ws, size_t ws_bytes, cslc_stream_t stream);
+
+/* Attention of one new token per sequence over the paged cache: query b sees
+ * the first n = min(seq_len[b], max_pages * P) tokens of sequence b, with
+ * window > 0 the last `window` of them. Tokens in pages that do not exist are
+ * skipped. What the cache holds behind token n has no influence.
+ *   o[b,h,:] = sum_j softmax_j(scale * q[b,h,:] . k_j) v_j
+ * over the stored values; fp32 statistics and accumulation, bf16 output. A
+ * sequence without a visible token outputs 0 and lse = -inf.
+ *
+ *   q [B, H, 128] bf16, q_stride elements from one sequence to the next
+ *   block_table [B, max_pages], seq_len [B] int32
+ *   out [B, H, 128] bf16; lse [B, H] fp32, or NULL
+ *   ws  workspace of cslc_page_decode_workspace_bytes() bytes; it belongs to
+ *       one call at a time (also in captured graphs)
+ * 0 <= B <= 8192, window >= 0. */
+size_t cslc_page_decode_workspace_bytes(int B, int H, int Hkv);
+cslc_status cslc_page_decode_attn(const cslc_bf16* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                  const float* k_scale, const float* v_scale, const int32_t* block_table,
+                                  const int32_t* seq_len, int B, int H, int Hkv, int D, int page, int n_pages,
+                                  int max_pages, int64_t q_stride, int window, float scale, cslc_bf16* out,
+                                  float* lse, void* ws, size_t ws_bytes, cslc_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* The decode top-k without a caller workspace (the source pages have no
  * counterpart: this is a deployment convenience of the library).
  *

@@ -1,0 +1,546 @@
+"""GPU parity of the paged serving operators (page plan, e4m3 cache write, prompt
+attention, decode attention over the cache) with the float64 paged oracle.
+
+Integers, codes and scales are equal. Attention: with u = 2^-8 (a bf16 rounding
+is off by at most half a step, eps / 2, relative), every output is
+
+    |err| <= u |o| + (u + 2 d + n 2^-24) a,      |err lse| <= d + n 2^-24 + 2^-23 |lse|
+
+with a = the softmax average of |v| (from the oracle), n the keys of the row: u |o|
+rounds the output, u a the probabilities, n 2^-24 the fp32 sums, and d bounds the
+error of a score and its exponential: 128 + 2 roundings to fp32 of sums of at most
+s = scale * sum |q||k| (from the oracle), and 2^-20 for exp2 and its argument.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_oracle as PO
+from tests.helpers import f64
+
+pytestmark = pytest.mark.gpu
+
+BF16, I32 = torch.bfloat16, torch.int32
+SCALE = 1 / math.sqrt(128)
+U = 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def C(cuda_device):
+    from compressed_sparse_long_compress_b200 import cslc
+    return cslc
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=I32, device="cuda")
+
+
+def randn(shape, seed, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(BF16)
+
+
+def check_attention(got, lse, ref, n, what=""):
+    o, l, a, s = ref
+    rows = ~np.isnan(l)
+    got, lse, o, l, a, s = f64(got)[rows], f64(lse)[rows], o[rows], l[rows], a[rows], s[rows]
+    d = s * 130 * 2.0 ** -24 + 2.0 ** -20
+    tol = U * np.abs(o) + (U + 2 * d + n * 2.0 ** -24)[..., None] * a
+    bad = ~(np.abs(got - o) <= tol + 1e-30)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} outputs, worst {np.nanmax(np.abs(got - o) - tol):.3e} beyond"
+    empty = np.isneginf(l)
+    assert np.array_equal(np.isneginf(lse), empty), what
+    e = np.abs(lse[~empty] - l[~empty])
+    tl = (d + n * 2.0 ** -24)[~empty] + 2.0 ** -23 * np.abs(l[~empty])
+    assert (e <= tl).all(), f"{what}: lse off by {e.max():.3e}, allowed {tl[e.argmax()]:.3e}"
+
+
+# ---------------------------------------------------------------- page plan
+
+def run_plan(C, old, new, free, table, page, n_pages, max_tokens):
+    got = i32(table)
+    slots, cu, n, st = C.page_plan(i32(old), i32(new), i32(free), got, page, n_pages, max_tokens=max_tokens)
+    ref = PO.page_plan(old, new, free, table, page, n_pages, max_tokens)
+    for g, r, name in zip((got, slots, cu, n, st), ref, ("table", "slots", "cu", "seq_len", "status")):
+        assert np.array_equal(g.cpu().numpy(), r), name
+    return got, slots, cu, n, st
+
+
+def plan_case(seed, B, max_old, max_new, page, extra=3, width=None):
+    r = np.random.RandomState(seed)
+    old, new = r.randint(0, max_old + 1, B), r.randint(0, max_new + 1, B)
+    p0, p1 = -(-old // page), -(-(old + new) // page)
+    n_pages = int(p1.sum()) + extra
+    pool = r.permutation(n_pages)
+    width = int(p1.max()) + 1 if width is None else width
+    table = np.full((B, width), -7)
+    at = 0
+    for b in range(B):
+        m = min(p0[b], width)
+        table[b, :m] = pool[at:at + m]
+        at += m
+    return old, new, pool[at:], table, n_pages
+
+
+@pytest.mark.parametrize("B,max_old,max_new,page", [(1, 0, 1, 16), (1, 100, 700, 64), (7, 50, 1, 128), (64, 300, 40, 32),
+                                                    (513, 90, 33, 16), (1500, 20, 2, 64)])
+def test_plan(C, B, max_old, max_new, page):
+    old, new, free, table, n_pages = plan_case(B + page, B, max_old, max_new, page)
+    run_plan(C, old, new, free, table, page, n_pages, int(new.sum()) + 9)
+
+
+def test_plan_runs_short_of_pages(C):
+    old, new, free, table, n_pages = plan_case(5, 40, 60, 70, 16)
+    need = int(PO.page_plan(old, new, free, table, 16, n_pages, 1)[4][0])
+    for k in (0, 1, need // 2, need - 1):
+        run_plan(C, old, new, free[:k], table, 16, n_pages, int(new.sum()))
+
+
+def test_plan_bad_pages_short_tables_and_few_slots(C):
+    old, new, free, table, n_pages = plan_case(6, 40, 60, 70, 16)
+    bad = free.copy()
+    bad[::3] = -1
+    bad[1::5] = n_pages + 4
+    run_plan(C, old, new, bad, table, 16, n_pages, int(new.sum()))
+    held = table.copy()
+    held[::2] = -1                                             # partly full pages that do not exist
+    run_plan(C, old, new, free, held, 16, n_pages, int(new.sum()))
+    run_plan(C, old, new, free, table[:, :3].copy(), 16, n_pages, int(new.sum()))
+    run_plan(C, old, new, free, table, 16, n_pages, int(new.sum()) // 3)
+    run_plan(C, old, new, free, table, 16, n_pages, 0)
+    neg = old.copy()
+    neg[:5] = -9
+    neg_new = new.copy()
+    neg_new[3:9] = -2
+    run_plan(C, neg, neg_new, free, np.abs(table), 16, n_pages, int(new.sum()))
+
+
+def test_plan_most_sequences_and_none(C):
+    old, new, free, table, n_pages = plan_case(8, 8192, 30, 3, 16)
+    run_plan(C, old, new, free, table, 16, n_pages, int(new.sum()) + 1)
+    e = np.zeros(0, dtype=np.int32)
+    run_plan(C, e, e, [1, 2], np.zeros((0, 3)), 16, 4, 5)
+
+
+def test_plan_large_lengths(C):
+    big = 2 ** 31 - 1
+    table = np.full((3, 2), -1)
+    run = C.page_plan(i32([big, 0, 5]), i32([0, 3, 0]), i32([4, 5]), i32(table), 64, 8, max_tokens=4)
+    assert run[0].tolist() == [256, 257, 258, -1] and run[3].tolist() == [1, 0]
+    assert run[1].tolist() == [0, 0, 3, 3] and run[2].tolist() == [big, 3, 5]
+
+
+# -------------------------------------------------------------- cache write
+
+def empty_cache(n_pages, Hkv, P, fill=0):
+    c = torch.full((n_pages, Hkv, P, 128), fill, dtype=torch.uint8, device="cuda")
+    return c, torch.full((n_pages, Hkv), 2.0 ** -5, device="cuda")
+
+
+def run_write(C, k, v, slots, kc, vc, ks, vs):
+    ref = [PO.page_write(f64(x), slots.cpu().numpy(), c.cpu().numpy(), f64(s)) for x, c, s in ((k, kc, ks), (v, vc, vs))]
+    C.page_write_e4m3(k, v, slots, kc, vc, ks, vs)
+    for (codes, scale), c, s, name in zip(ref, (kc, vc), (ks, vs), "kv"):
+        assert np.array_equal(f64(s), scale), name
+        assert np.array_equal(c.cpu().numpy(), codes), name
+
+
+@pytest.mark.parametrize("P", [16, 32, 64, 128])
+@pytest.mark.parametrize("Hkv,lens", [(1, [1]), (3, [5, 130, 1, 64]), (8, [1] * 33), (2, [127, 128, 129, 300])])
+def test_write_ragged(C, P, Hkv, lens):
+    r = np.random.RandomState(P + Hkv)
+    old = r.randint(0, 2 * P, len(lens))
+    p0, p1 = -(-old // P), -(-(old + lens) // P)
+    n_pages = int(p1.sum()) + 2
+    pool = r.permutation(n_pages)
+    table, at = np.full((len(lens), int(p1.max())), -1), 0
+    for b in range(len(lens)):
+        table[b, :p0[b]] = pool[at:at + p0[b]]
+        at += p0[b]
+    _, slots, _, _, _ = run_plan(C, old, lens, pool[at:], table, P, n_pages, sum(lens) + 3)
+    kc, ks = empty_cache(n_pages, Hkv, P, 0x31)
+    vc, vs = empty_cache(n_pages, Hkv, P, 0xC5)
+    kv = randn((slots.numel(), 2, Hkv, 128), 40 + P)             # one fused projection: rows lie apart
+    for step in range(3):                                        # the same slots again, smaller and larger values
+        x = kv * [1.0, 0.01, 300.0][step]
+        run_write(C, x[:, 0], x[:, 1], slots, kc, vc, ks, vs)
+
+
+def test_write_extremes(C):
+    P, Hkv = 16, 2
+    kc, ks = empty_cache(8, Hkv, P)
+    vc, vs = empty_cache(8, Hkv, P)
+    k, v = randn((40, Hkv, 128), 1), randn((40, Hkv, 128), 2)
+    k[0, 0, :4] = torch.tensor([math.inf, -math.inf, math.nan, 5.0])
+    k[1:16, 1] = 0.0                                             # zeros but for one value
+    k[17:21] = math.nan                                          # a run of NaN only: no finite value
+    k[22:30] *= 1e30                                             # above the largest scale
+    v[:16] *= 1e-30                                              # below the smallest
+    v[16:21] = math.inf
+    v[21:40] = torch.finfo(BF16).max
+    slots = i32(list(range(16, 32)) + [0, 1, 2, 3, 4] + list(range(40, 48)) + [-1, 8 * 16, 2 ** 31 - 1, -2 ** 31] +
+                list(range(64, 71)))
+    run_write(C, k, v, slots, kc, vc, ks, vs)
+    run_write(C, v, k, slots, kc, vc, ks, vs)
+
+
+def test_write_moves_every_code_to_every_scale(C):
+    """Codes before the run, all 256 of them, to scales 2^1 .. 2^14 larger."""
+    P, shifts = 16, list(range(1, 15)) + [40, 60]
+    n = len(shifts)
+    codes = torch.arange(256, dtype=torch.uint8, device="cuda").repeat(8).view(1, 1, 16, 128)
+    kc = codes.expand(n, 1, 16, 128).contiguous()
+    vc, (_, vs) = kc.clone(), empty_cache(n, 1, P)
+    ks = torch.full((n, 1), 2.0 ** -20, device="cuda")
+    k = torch.zeros(n, 1, 128, dtype=BF16, device="cuda")
+    k[:, 0, 5] = torch.tensor([448.0 * 2.0 ** (s - 20) for s in shifts], dtype=BF16)
+    run_write(C, k, k, i32([i * P + 15 for i in range(n)]), kc, vc, ks, vs)
+
+
+def test_write_nothing(C):
+    kc, ks = empty_cache(3, 2, 16)
+    k = randn((4, 2, 128), 3)
+    run_write(C, k, k, i32([-1] * 4), kc, kc.clone(), ks, ks.clone())
+    C.page_write_e4m3(k[:0], k[:0], i32([]), kc, kc, ks, ks)
+
+
+# --------------------------------------------------------- prompt attention
+
+def run_prompt(C, nq, nk, H, Hkv, window=0, seed=0, scale=SCALE, lead=0, tail=0, edit=None, rows=None):
+    """Packed sequences, `lead` and `tail` rows of no sequence; q, k, v are views of one fused projection."""
+    Tq, Tk = sum(nq) + lead + tail, sum(nk) + lead + tail
+    T = max(Tq, Tk)
+    qkv = randn((T, H + 2 * Hkv, 128), 100 + seed)
+    q, k, v = qkv[:Tq, :H], qkv[:Tk, H:H + Hkv], qkv[:Tk, H + Hkv:]
+    if edit:
+        edit(q, k, v)
+    cu_q, cu_k = np.concatenate([[0], np.cumsum(nq)]) + lead, np.concatenate([[0], np.cumsum(nk)]) + lead
+    out = torch.full((Tq, H, 128), 7.0, dtype=BF16, device="cuda")
+    lse = torch.full((Tq, H), 9.0, device="cuda")
+    C.prompt_attn(q, k, v, i32(cu_q), i32(cu_k), scale, window, out=out, lse=lse)
+    C.sync_status()
+    ref = PO.prompt_attention(f64(q), f64(k), f64(v), cu_q, cu_k, scale, window, rows=rows)
+    if rows is None:
+        none = np.isnan(ref[1][:, 0]) & (np.arange(Tq) >= 0)
+        none[lead:Tq - tail if tail else Tq] = False
+        assert (f64(out)[none] == 7).all() and (f64(lse)[none] == 9).all()
+    check_attention(out, lse, ref, max(nk + [1]), f"nq {nq} nk {nk} H {H}/{Hkv} window {window}")
+    return out, lse
+
+
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (2, 2), (3, 1), (8, 2), (16, 2), (10, 2), (7, 1), (12, 1), (48, 8), (64, 8)])
+def test_prompt_heads(C, H, Hkv):
+    run_prompt(C, [1, 67, 33], [1, 67, 40], H, Hkv, seed=H)
+
+
+@pytest.mark.parametrize("H,Hkv", [(33, 1), (96, 1), (128, 1), (128, 128)])
+def test_prompt_extreme_heads(C, H, Hkv):
+    run_prompt(C, [9, 14], [9, 30], H, Hkv, seed=H)
+
+
+@pytest.mark.parametrize("nq,nk", [([1], [1]), ([1], [129]), ([2], [1000]), ([127], [127]), ([128], [128]), ([129], [129]),
+                                   ([255, 1, 257], [255, 1, 257]), ([300], [600]), ([64, 0, 5, 0], [64, 0, 5, 70]),
+                                   ([5, 9, 40], [0, 3, 40])])
+def test_prompt_lengths(C, nq, nk):
+    run_prompt(C, nq, nk, 4, 2, seed=len(nq) + nq[0])
+
+
+@pytest.mark.parametrize("window", [1, 2, 63, 64, 127, 128, 129, 200, 100000])
+def test_prompt_window(C, window):
+    run_prompt(C, [290, 40], [290, 170], 8, 2, window=window, seed=window % 97)
+
+
+def test_prompt_rows_of_no_sequence(C):
+    run_prompt(C, [40, 3], [40, 60], 8, 2, lead=5, tail=21, seed=3)
+    run_prompt(C, [0, 0], [4, 0], 4, 4, tail=130, seed=4)
+
+
+def test_prompt_many_short_sequences(C):
+    r = np.random.RandomState(2)
+    nq = r.randint(0, 4, 600).tolist()
+    run_prompt(C, nq, [n + int(e) for n, e in zip(nq, r.randint(0, 3, 600))], 4, 1, seed=9)
+
+
+@pytest.mark.parametrize("grow", [3.0, 40.0])
+def test_prompt_scores_that_grow(C, grow):
+    """Later keys score far higher (the running reference has to move) or lower."""
+    def edit(q, k, v):
+        d = torch.linspace(-1, 1, k.shape[0], device="cuda")[:, None, None]
+        k.copy_((k + grow * d * torch.sign(k[:1])).to(BF16))
+    run_prompt(C, [400], [400], 4, 2, seed=1, edit=edit)
+    run_prompt(C, [200, 150], [400, 150], 4, 2, seed=2, edit=lambda q, k, v: (edit(q, k, v), q.mul_(4)), window=90)
+
+
+def test_prompt_what_is_not_seen_has_no_influence(C):
+    """NaN and infinities in keys and values that a row does not see: after the
+    causal edge, before the window, in other sequences and behind the last."""
+    nq, H, Hkv, w = [150, 90], 8, 2, 40
+    clean = {}
+
+    def edit(q, k, v):
+        clean.update(q=q.clone(), k=k.clone(), v=v.clone())
+        for x, at in ((k, 100), (v, 100), (k, 3), (v, 3), (v, 149)):
+            x[at, 0, ::7] = math.nan
+            x[at, 1, 1::5] = math.inf
+            x[at, 1, 2::5] = -math.inf
+        k[240:], v[240:] = math.nan, math.nan
+
+    T = 240 + 30
+    qkv = randn((T, H + 2 * Hkv, 128), 55)
+    q, k, v = qkv[:, :H], qkv[:, H:H + Hkv], qkv[:, H + Hkv:]
+    edit(q, k, v)
+    cu = np.array([0, 150, 240])
+    for window in (0, w):
+        out, lse = C.prompt_attn(q, k, v, i32(cu), i32(cu), SCALE, window, lse=True)
+        C.sync_status()
+        ref = PO.prompt_attention(f64(clean["q"]), f64(clean["k"]), f64(clean["v"]), cu, cu, SCALE, window)
+        i = np.arange(240)
+        lo = np.maximum(np.where(i < 150, 0, 150), i - (window - 1 if window else 10 ** 6))
+        sees = lambda at: (lo <= at) & (at <= i)  # noqa: E731
+        touched = sees(100) | sees(3) | sees(149)
+        for x in ref:
+            x[:240][touched] = np.nan
+        assert (~touched).sum() > 90
+        check_attention(out, lse, ref, 150, f"window {window}")
+        got = f64(out)[:240]
+        assert np.isnan(got[sees(100)][:, :, ::7]).any(axis=2).all()       # rows that do see them
+
+
+def test_prompt_infinite_value_is_infinite_where_it_is_seen(C):
+    q, k, v = randn((200, 2, 128), 1), randn((200, 1, 128), 2), randn((200, 1, 128), 3)
+    v[130, 0, 5], v[131, 0, 9] = math.inf, -math.inf
+    cu = i32([0, 200])
+    out, _ = C.prompt_attn(q, k, v, cu, cu, SCALE)
+    o = f64(out)
+    assert np.isfinite(o[:130]).all() and np.isposinf(o[130:, :, 5]).all() and np.isneginf(o[131:, :, 9]).all()
+    o[130:, :, 5], o[131:, :, 9] = 0, 0
+    assert np.isfinite(o).all()
+
+
+def test_prompt_masked_by_the_lowest_value(C):
+    """Keys whose scores are the lowest finite values next to plain ones, and alone."""
+    q, k, v = randn((64, 2, 128), 4), randn((64, 1, 128), 5), randn((64, 1, 128), 6)
+    q[:, :, 0], k[:, :, 0] = 1.0, 0.0
+    k[::2, :, 0] = torch.finfo(BF16).min
+    cu = i32([0, 64])
+    out, lse = C.prompt_attn(q, k, v, cu, cu, 1.0, lse=True)
+    C.sync_status()
+    o, l, a, s = PO.prompt_attention(f64(q), f64(k), f64(v), [0, 64], [0, 64], 1.0)
+    got = f64(out)
+    assert np.isfinite(got).all() and np.isfinite(f64(lse)).all()
+    # row 0 sees only such a key; the later ones ignore them: their scores' products are small
+    assert np.abs(got[0] - f64(v)[0]).max() <= U * np.abs(f64(v)[0]).max()
+    plain = PO.prompt_attention(f64(q)[1:], f64(k)[1::2], f64(v)[1::2], [0, 63], [0, 32], 1.0)[0]
+    for t in (1, 2, 3, 40, 63):
+        j = np.arange(1, t + 1, 2)
+        ref = PO.attend_rows(f64(q)[t], f64(k)[j, 0], f64(v)[j, 0], 1.0)
+        assert (np.abs(got[t] - ref[0]) <= U * np.abs(ref[0]) + (U + 2.0 ** -14) * ref[2]).all()
+    assert plain.shape == (63, 2, 128)
+
+
+def test_prompt_long_rows_sampled(C):
+    rows = {0, 1, 500, 4000, 5200, 5201, 5202, 9000, 9300, 9301}
+    run_prompt(C, [5201, 4101], [5201, 4101], 8, 1, seed=77, rows=rows)
+
+
+# --------------------------------------------------------- decode attention
+
+def make_cache(n_pages, Hkv, P, seed, spread=3):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    shape = (n_pages, Hkv, P, 128)
+    codes = [(torch.randn(shape, device="cuda", generator=g) * 120).clamp(-448, 448).to(torch.float8_e4m3fn)
+             .view(torch.uint8) for _ in range(2)]
+    scales = [torch.ldexp(torch.ones(n_pages, Hkv, device="cuda"),
+                          torch.randint(-8 - spread, -5, (n_pages, Hkv), device="cuda", generator=g)) for _ in range(2)]
+    return codes + scales
+
+
+def run_decode(C, lens, H, Hkv, P, window=0, seed=0, q_std=1.0, spread=3, cache=None, bad=(), width=None):
+    r = np.random.RandomState(seed + 7 * H + P)
+    pages = [-(-max(n, 0) // P) for n in lens]
+    n_pages = sum(pages) + 3
+    cache = make_cache(n_pages, Hkv, P, seed + 200, spread) if cache is None else cache
+    pool = r.permutation(n_pages)
+    width = max(pages + [1]) + 1 if width is None else width
+    table, at = np.full((len(lens), width), n_pages + 99), 0
+    for b, m in enumerate(pages):
+        table[b, :min(m, width)] = pool[at:at + min(m, width)]
+        at += m
+    for b, j, p in bad:
+        table[b, j] = p
+    q = randn((len(lens), H + 2, 128), seed, q_std)[:, :H]
+    out, lse = C.page_decode_attn(q, *cache, i32(table), i32(lens), SCALE, window, lse=True)
+    C.sync_status()
+    kc, vc, ks, vs = (x.cpu().numpy() for x in cache)
+    ref = PO.page_decode_attention(f64(q), kc, vc, ks.astype(np.float64), vs.astype(np.float64), table, lens, SCALE, window)
+    check_attention(out, lse, ref, max(lens), f"lens {lens} H {H}/{Hkv} P {P} window {window}")
+    return out, lse
+
+
+@pytest.mark.parametrize("P", [16, 32, 64, 128])
+@pytest.mark.parametrize("lens", [[1], [0], [17, 0, 1, 300], [127, 128, 129, 255, 256, 257], [1500]])
+def test_decode_lengths(C, P, lens):
+    run_decode(C, lens, 8, 2, P, seed=len(lens))
+
+
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (4, 4), (5, 1), (8, 1), (9, 1), (16, 1), (12, 2), (17, 1), (64, 8), (32, 1),
+                                   (40, 1), (128, 2), (128, 1), (128, 128)])
+def test_decode_heads(C, H, Hkv):
+    run_decode(C, [70, 5, 333], H, Hkv, 64, seed=H)
+
+
+@pytest.mark.parametrize("window", [1, 15, 64, 100, 129, 5000])
+@pytest.mark.parametrize("P", [16, 128])
+def test_decode_window(C, window, P):
+    run_decode(C, [3, 200, 777, 130], 8, 2, P, window=window, seed=window)
+
+
+def test_decode_many_sequences(C):
+    r = np.random.RandomState(4)
+    run_decode(C, r.randint(0, 90, 400).tolist(), 4, 1, 16, seed=2)
+
+
+def test_decode_long_context(C):
+    run_decode(C, [20001, 3, 9000], 4, 2, 64, seed=5)
+
+
+@pytest.mark.parametrize("q_std", [0.0, 0.01, 8.0, 60.0])
+def test_decode_flat_and_peaked(C, q_std):
+    run_decode(C, [900, 40], 8, 2, 32, seed=6, q_std=q_std)
+
+
+def test_decode_scales_far_apart(C):
+    """Pages whose scales differ by up to 2^30: neither values nor weights get lost."""
+    run_decode(C, [700, 129], 8, 2, 16, seed=8, spread=30)
+
+
+def test_decode_pages_that_do_not_exist(C):
+    run_decode(C, [100, 200, 50], 8, 2, 16, seed=9, bad=[(0, 2, -1), (1, 0, 10 ** 6), (1, 11, -2 ** 31), (2, 0, -1), (2, 1, -1),
+                                                         (2, 2, -1), (2, 3, 2 ** 31 - 1)])
+    run_decode(C, [1000, 40], 8, 2, 16, seed=10, width=5)               # longer than its table
+    run_decode(C, [-5, 40], 8, 2, 16, seed=11)
+
+
+def test_decode_stale_pages_have_no_influence(C):
+    """NaN codes behind a sequence's end, before its window and in pages of nobody."""
+    P, lens = 64, [70, 129, 64, 1]
+    cache = make_cache(12, 2, P, 77)
+    table = np.array([[3, 0, 11], [5, 6, 2], [1, 11, 11], [8, 11, 11]])
+    q = randn((4, 8, 128), 5)
+    for window in (0, 40):
+        kc, vc, ks, vs = (x.clone() for x in cache)
+        ref = PO.page_decode_attention(f64(q), kc.cpu().numpy(), vc.cpu().numpy(), f64(ks), f64(vs), table, lens, SCALE, window)
+        for b, n in enumerate(lens):
+            lo = max(0, n - window) if window else 0
+            for x in list(range(0, lo)) + list(range(n, 3 * P)):
+                p = table[b, x // P]
+                if p != 11:
+                    kc[p, :, x % P], vc[p, :, x % P] = 0x7F, 0xFF
+        for p in (4, 7, 9, 10, 11):
+            kc[p], vc[p] = 0x7F, 0x7F
+            ks[p], vs[p] = math.nan, math.inf
+        out, lse = C.page_decode_attn(q, kc, vc, ks, vs, i32(table), i32(lens), SCALE, window, lse=True)
+        C.sync_status()
+        check_attention(out, lse, ref, 129, f"window {window}")
+
+
+def test_decode_nan_code_that_is_seen(C):
+    cache = make_cache(4, 1, 64, 3)
+    cache[1][2, 0, 10, 5] = 0x7F
+    out, _ = C.page_decode_attn(randn((2, 4, 128), 1), *cache, i32([[2, 1], [3, 1]]), i32([100, 100]), SCALE)
+    o = f64(out)
+    assert np.isnan(o[0, :, 5]).all() and np.isfinite(np.delete(o[0], 5, axis=1)).all() and np.isfinite(o[1]).all()
+
+
+# --------------------------------------------------------------- a run of them
+
+def test_serving_run(C):
+    """Prompts of different lengths are planned, written and attended to, then
+    decoded for 40 steps; one step is captured and replayed. Every output equals
+    the oracle's on the cache's own content, and the cache equals the oracle's."""
+    P, H, Hkv, B, n_pages, width = 16, 8, 2, 3, 40, 12
+    lens = [37, 1, 90]
+    cache = [torch.zeros(n_pages, Hkv, P, 128, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cache += [torch.zeros(n_pages, Hkv, device="cuda") for _ in range(2)]
+    table = i32(np.full((B, width), -1))
+    free = i32(np.random.RandomState(1).permutation(n_pages))
+    T = sum(lens)
+    q, k, v = randn((T, H, 128), 1), randn((T, Hkv, 128), 2), randn((T, Hkv, 128), 3)
+    slots, cu, n, st = C.page_plan(i32([0] * B), i32(lens), free, table, P, n_pages, max_tokens=T)
+    C.page_write_e4m3(k, v, slots, *cache)
+    out, lse = C.prompt_attn(q, k, v, cu, cu, SCALE, lse=True)
+    check_attention(out, lse, PO.prompt_attention(f64(q), f64(k), f64(v), cu.tolist(), cu.tolist(), SCALE), max(lens))
+    used = st.tolist()[0]
+    assert st.tolist()[1] == 0 and n.tolist() == lens
+
+    def np_cache():
+        return [x.cpu().numpy().astype(x.cpu().numpy().dtype if x.dtype == torch.uint8 else np.float64) for x in cache]
+
+    one = i32([1] * B)
+    free_now = torch.zeros(B, dtype=I32, device="cuda")
+    held = n.clone()
+    q1, k1, v1 = randn((B, H, 128), 4), randn((B, Hkv, 128), 5), randn((B, Hkv, 128), 6)
+    bufs = dict(slots=torch.empty(B, dtype=I32, device="cuda"), cu=torch.empty(B + 1, dtype=I32, device="cuda"),
+                seq_len=torch.empty(B, dtype=I32, device="cuda"), status=torch.empty(2, dtype=I32, device="cuda"))
+    o1, l1 = torch.empty_like(q1), torch.empty(B, H, device="cuda")
+    ws = torch.empty(max(16, C.page_decode_workspace_bytes(B, H, Hkv)), dtype=torch.uint8, device="cuda")
+
+    def step():
+        C.page_plan(held, one, free_now, table, P, n_pages, **bufs)
+        C.page_write_e4m3(k1, v1, bufs["slots"], *cache)
+        C.page_decode_attn(q1, *cache, table, bufs["seq_len"], SCALE, out=o1, lse=l1, ws=ws)
+
+    graph = None
+    for i in range(40):
+        free_now.copy_(free[used:used + B])
+        q1.copy_(randn((B, H, 128), 100 + i))
+        k1.copy_(randn((B, Hkv, 128), 200 + i) * (1 + i // 8))
+        v1.copy_(randn((B, Hkv, 128), 300 + i) * (1 + i // 8))
+        before = np_cache()
+        if i < 3:
+            step()
+        else:
+            if graph is None:
+                side = torch.cuda.Stream()
+                side.wait_stream(torch.cuda.current_stream())
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph, stream=side):
+                    step()
+            graph.replay()
+        torch.cuda.synchronize()
+        after, sl = np_cache(), bufs["slots"].cpu().numpy()
+        for x, c in ((k1, 0), (v1, 1)):
+            codes, scale = PO.page_write(f64(x), sl, before[c], before[2 + c])
+            assert np.array_equal(codes, after[c]) and np.array_equal(scale, after[2 + c]), i
+        ref = PO.page_decode_attention(f64(q1), after[0], after[1], after[2], after[3], table.cpu().numpy(),
+                                       bufs["seq_len"].tolist(), SCALE)
+        check_attention(o1, l1, ref, 200, f"step {i}")
+        assert bufs["status"].tolist()[1] == 0
+        used += bufs["status"].tolist()[0]
+        held.copy_(bufs["seq_len"])
+    C.sync_status()
+
+
+def test_calls_on_other_streams_and_repeated(C):
+    """Two streams at once, each call twice: the same bits."""
+    T, H, Hkv = 700, 8, 2
+    q, k, v = randn((T, H, 128), 1), randn((T, Hkv, 128), 2), randn((T, Hkv, 128), 3)
+    cu = i32([0, 123, 700])
+    cache = make_cache(60, Hkv, 64, 4)
+    table, n = i32(np.random.RandomState(1).randint(0, 60, (9, 30))), i32([1900, 5, 0, 64, 65, 700, 1, 1920, 333])
+    want = C.prompt_attn(q, k, v, cu, cu, SCALE, lse=True), C.page_decode_attn(q[:9], *cache, table, n, SCALE, lse=True)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(6):
+        for s in streams:
+            got.append((C.prompt_attn(q, k, v, cu, cu, SCALE, lse=True, stream=s),
+                        C.page_decode_attn(q[:9], *cache, table, n, SCALE, lse=True, stream=s)))
+    torch.cuda.synchronize()
+    C.sync_status()
+    for g in got:
+        for a, b in zip(g, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
