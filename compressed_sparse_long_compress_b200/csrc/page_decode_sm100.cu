@@ -1,0 +1,633 @@
+// Attention of one new token per sequence over the paged e4m3 cache, on the
+// 5th-generation tensor cores (tcgen05 + TMEM).
+//
+// Mathematics. A tile is 128 consecutive tokens of a sequence; a unit is one
+// (sequence, key head, group of up to GP query heads). The codes are operands
+// as they lie in the cache, without a conversion:
+//   S^T[token, head] = K[token, dim] q[head, dim]       (M = 128 tokens)
+//   O^T[dim, head]   = V^T[dim, token] P[token, head]   (M = 128 dims; V MN-major)
+// q and P have 8 significant bits and e4m3 has 4, so each is split into two
+// e4m3 parts that sit side by side as N = 2 GP columns: x = hi + lo / 16, hi =
+// e4m3(x), lo = e4m3(16 (x - hi)). For q (scaled by a power of two to [128,
+// 256) at its largest) the split is exact; for P it is what a rounding to bf16
+// would be (2^-8). Page scales are powers of two: k's multiplies the score, v's
+// is added to the score's exponent before the exponential, so P V needs no
+// scale of its own, and is taken out again (times 2^-e) for the softmax sum.
+// Each tile has its own reference (its exact maximum, mapped to 2^8): the O^T of
+// a tile is a fresh product, rescaled as it joins the fp32 sum in registers.
+// So a probability is off by at most 2^-22 of the largest one of its own tile,
+// however flat and long the tail is; a running reference would lose tails of
+// 2^-23 per token.
+//
+// Work. All tiles of all units, in the order of the sequences, are dealt to the
+// CTAs in equal consecutive ranges (two CTAs per SM), whatever the lengths are.
+// A unit that crosses CTAs leaves fp32 partials in the workspace, which
+// page_decode_combine_kernel (a programmatic dependent launch) merges.
+//
+// CTA roles: warps 0-3 softmax (thread = token, then = dim), warp 4 producer
+// (page table and scales, one tile ahead; TMA of each page's codes, STAGES-deep
+// ring), warp 5 TMEM allocation and the MMA-issuing thread. Tokens outside
+// the sequence's visible range get P = 0 and their V rows are cleared in shared memory,
+// since stale codes may be NaN. All waits are time-bounded.
+
+#include "sm100.cuh"
+
+namespace cslc {
+
+using namespace sm100;
+
+__device__ int g_page_decode_err = 0;
+
+namespace {
+
+constexpr int PD_THREADS = 192;
+constexpr int PD_PROD_WARP = 4;
+constexpr int PD_MMA_WARP = 5;
+constexpr int PD_TILE = 128;
+constexpr int PD_STAGES = 3;
+constexpr int PD_HALF = PD_TILE * 128;        // 16 KB: K or V codes of a tile
+constexpr int PD_CTAS = 296;                  // two per SM on 148 SMs
+
+enum { PD_ERR_EMPTY = 1, PD_ERR_K_FULL, PD_ERR_V_FULL, PD_ERR_Q_FULL, PD_ERR_S_FULL, PD_ERR_P_FULL, PD_ERR_O_FULL,
+       PD_ERR_FINAL };
+
+struct __align__(8) PdBars {
+  uint64_t k_full[PD_STAGES], v_full[PD_STAGES], empty[PD_STAGES];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t q_full, final_bar;
+};
+
+template <int GP>
+struct PdSmall {
+  PdBars bars;
+  float ks[PD_STAGES][8];                     // scale of each page of the tile's keys
+  int ev[PD_STAGES][8];                       // exponent of its values' scale; PD_ABSENT: no such page
+  __align__(16) float smax[2][GP][4];         // a tile's maxima by warp
+  float lsum[GP][4];
+  float qs[GP];                               // what a score of the parts' products is multiplied with
+  long long scan[PD_THREADS / 32];
+  long long x_pre;                            // tiles before sequence x_b
+  int x_b;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+constexpr int PD_ABSENT = 1 << 20;
+
+struct PdShape {
+  int B, H, Hkv, G, HG, page_log2, n_pages, max_pages, window;
+  float scale_log2;
+  long long q_stride;
+};
+
+// Visible tokens of sequence b: [lo, n); its tiles: [lo / 128, ceil(n / 128)).
+__device__ __forceinline__ int pd_range(const PdShape& sh, const int32_t* __restrict__ seq_len, int b, int& lo, int& t0) {
+  const long long cap = (long long)sh.max_pages << sh.page_log2;
+  const int n = (int)min((long long)max(seq_len[b], 0), cap);
+  lo = sh.window > 0 ? max(0, n - sh.window) : 0;
+  t0 = lo / PD_TILE;
+  return n;
+}
+__device__ __forceinline__ int pd_tiles(const PdShape& sh, const int32_t* __restrict__ seq_len, int b) {
+  int lo, t0;
+  const int n = pd_range(sh, seq_len, b, lo, t0);
+  return (n + PD_TILE - 1) / PD_TILE - t0;
+}
+
+// Walks a CTA's range [x, x1) of the tiles, a segment (tiles of one unit) at a time.
+struct PdWalk {
+  long long x, x1, pre;                       // pre: tiles before sequence b (over one unit each)
+  int b;
+  // the segment: tiles t .. t + len - 1 of the nt tiles of unit u of sequence b
+  int u, t, len, nt;
+  __device__ __forceinline__ bool next(const PdShape& sh, const int32_t* __restrict__ seq_len) {
+    if (x >= x1) return false;
+    const int HU = sh.Hkv * sh.HG;
+    while (true) {
+      nt = pd_tiles(sh, seq_len, b);
+      if (x < (pre + nt) * HU) break;
+      pre += nt;
+      ++b;
+    }
+    const long long off = x - pre * HU;
+    u = (int)(off / nt);
+    t = (int)(off - (long long)u * nt);
+    len = (int)min((long long)(nt - t), x1 - x);
+    x += len;
+    return true;
+  }
+};
+
+}  // namespace
+
+// Partials in the workspace: per CTA a header of 8 ints, then per slot (two per
+// CTA: its first segment, its last one) GP x 128 sums and GP (reference, sum).
+struct PdWs {
+  int* hdr;       // [PD_CTAS][8]: b, u, t, nt, tiles per CTA (two words); b = -1 when no unit continues here
+  float* o;       // [2 PD_CTAS][GP][128]
+  float2* rl;     // [2 PD_CTAS][GP]
+};
+
+template <int GP>
+__global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
+    PdShape sh, const uint16_t* __restrict__ q, const float* __restrict__ k_scale, const float* __restrict__ v_scale,
+    const int32_t* __restrict__ table, const int32_t* __restrict__ seq_len, uint16_t* __restrict__ out,
+    float* __restrict__ lse, PdWs ws, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+  constexpr int N = 2 * GP;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* kv_s = smem;                                   // [STAGES][K 16 KB | V 16 KB]
+  uint8_t* q_s = kv_s + PD_STAGES * 2 * PD_HALF;          // [N][128 B]
+  uint8_t* p_s = q_s + N * 128;                           // [2][N][128 B]
+  PdSmall<GP>* sm = reinterpret_cast<PdSmall<GP>*>(p_s + 2 * N * 128);
+  PdBars& bars = sm->bars;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int HU = sh.Hkv * sh.HG;
+
+  if (tid == 0) {
+    for (int s = 0; s < PD_STAGES; ++s) {
+      mbar_init(&bars.k_full[s], 1); mbar_init(&bars.v_full[s], 1); mbar_init(&bars.empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) { mbar_init(&bars.s_full[i], 1); mbar_init(&bars.p_full[i], 4); mbar_init(&bars.o_full[i], 1); }
+    mbar_init(&bars.q_full, 4);
+    mbar_init(&bars.final_bar, 1);
+    sm->abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == PD_MMA_WARP) tmem_alloc(&sm->tmem_base, 4 * N < 32 ? 32 : 4 * N);
+
+  // ---- this CTA's range of the tiles: a scan of the sequences' tile counts
+  long long x0, x1, per;
+  {
+    const int each = (sh.B + PD_THREADS - 1) / PD_THREADS;
+    const int b0 = min(sh.B, tid * each), b1 = min(sh.B, b0 + each);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) sum += pd_tiles(sh, seq_len, b);
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) sm->scan[warp] = incl;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < PD_THREADS / 32; ++w) {
+      if (w < warp) incl += sm->scan[w];
+      total += sm->scan[w];
+    }
+    total *= HU;
+    per = (total + gridDim.x - 1) / gridDim.x;
+    x0 = min(total, per * blockIdx.x);
+    x1 = min(total, x0 + per);
+    // the thread whose sequences hold tile x0 finds the sequence
+    if (x0 < x1 && x0 >= (incl - sum) * HU && x0 < incl * HU) {
+      long long pre = incl - sum;
+      int b = b0;
+      while (true) {
+        const int nt = pd_tiles(sh, seq_len, b);
+        if (x0 < (pre + nt) * HU) break;
+        pre += nt;
+        ++b;
+      }
+      sm->x_pre = pre;
+      sm->x_b = b;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm->tmem_base;
+  volatile int* abortp = &sm->abort_flag;
+  int* errp = &g_page_decode_err;
+  PdWalk walk;
+  walk.x = x0; walk.x1 = x1; walk.pre = x0 < x1 ? sm->x_pre : 0; walk.b = x0 < x1 ? sm->x_b : 0;
+
+  if (warp == PD_PROD_WARP) {
+    // ------------------------------------------------------------ producer
+    const int ppt = PD_TILE >> sh.page_log2;               // pages of a tile, at most 8
+    const int P = 1 << sh.page_log2;
+    if (lane == 0) { tma_prefetch_map(&tm_k); tma_prefetch_map(&tm_v); }
+    int it = 0;
+    bool ok = true;
+    // lane i < ppt holds page i of the tile; the next tile's entry and scales
+    // are loaded before this tile's wait
+    auto load = [&](int b, int u, int lo, int n, int tile, int& y, float& ks, int& ev) {
+      y = -1; ks = 0.f; ev = PD_ABSENT;
+      if (lane < ppt) {
+        const long long j = (long long)tile * ppt + lane;
+        const long long tok = j << sh.page_log2;
+        if (tok < n && tok + P > lo) {
+          const int pid = table[(size_t)b * sh.max_pages + j];
+          if (pid >= 0 && pid < sh.n_pages) {
+            const int hk = u / sh.HG;
+            const size_t ps = (size_t)pid * sh.Hkv + hk;
+            y = (int)(ps << sh.page_log2);
+            ks = k_scale[ps];
+            ev = min(max((int)((__float_as_uint(v_scale[ps]) >> 23) & 0xff) - 127, -40), 60);
+          }
+        }
+      }
+    };
+    while (ok && walk.next(sh, seq_len)) {
+      int lo, t0;
+      const int n = pd_range(sh, seq_len, walk.b, lo, t0);
+      int y, ev;
+      float ks;
+      load(walk.b, walk.u, lo, n, t0 + walk.t, y, ks, ev);
+      for (int i = 0; i < walk.len; ++i, ++it) {
+        const int s = it % PD_STAGES;
+        int y2 = -1, ev2 = PD_ABSENT;
+        float ks2 = 0.f;
+        if (i + 1 < walk.len) load(walk.b, walk.u, lo, n, t0 + walk.t + i + 1, y2, ks2, ev2);
+        if (it >= PD_STAGES) {
+          bool w = true;
+          if (lane == 0) w = mbar_wait(&bars.empty[s], (uint32_t)((it / PD_STAGES - 1) & 1), abortp, errp, PD_ERR_EMPTY);
+          ok = __shfl_sync(0xffffffffu, (int)w, 0) != 0;
+          if (!ok) break;
+        }
+        if (lane < ppt) { sm->ks[s][lane] = ks; sm->ev[s][lane] = ev; }
+        __syncwarp();
+        if (lane == 0) { mbar_arrive_expect_tx(&bars.k_full[s], PD_HALF); mbar_arrive_expect_tx(&bars.v_full[s], PD_HALF); }
+        __syncwarp();
+        // a page that is not there reads the zero fill (a row past the end)
+        if (lane < ppt) {
+          const int row = y >= 0 ? y : max(1, (int)(((long long)sh.n_pages * sh.Hkv) << sh.page_log2));
+          uint8_t* dst = kv_s + s * 2 * PD_HALF + (lane << sh.page_log2) * 128;
+          tma_load_2d(dst, &tm_k, 0, row, &bars.k_full[s]);
+          tma_load_2d(dst + PD_HALF, &tm_v, 0, row, &bars.v_full[s]);
+        }
+        y = y2; ks = ks2; ev = ev2;
+      }
+    }
+    // loads in flight after an abort land before the CTA leaves
+    if (lane == 0)
+      for (int d = 1; d <= PD_STAGES && it - d >= 0; ++d) {
+        const int k2 = it - d;
+        mbar_wait_done(&bars.k_full[k2 % PD_STAGES], (uint32_t)((k2 / PD_STAGES) & 1), errp, PD_ERR_K_FULL);
+        mbar_wait_done(&bars.v_full[k2 % PD_STAGES], (uint32_t)((k2 / PD_STAGES) & 1), errp, PD_ERR_V_FULL);
+      }
+    __syncwarp();
+  } else if (warp == PD_MMA_WARP) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t ID_S = idesc_e4m3(128, N);
+      constexpr uint32_t ID_O = idesc_e4m3(128, N) | (1u << 15);   // A = V^T, MN-major
+      int it = 0, seg = 0;
+      bool ok = true;
+      const uint32_t q0 = smem_u32(q_s);
+      auto issue_pv = [&](int j) -> bool {
+        const int s = j % PD_STAGES, pb = j & 1;
+        if (!mbar_wait(&bars.p_full[pb], (uint32_t)((j >> 1) & 1), abortp, errp, PD_ERR_P_FULL)) return false;
+        if (!mbar_wait(&bars.v_full[s], (uint32_t)((j / PD_STAGES) & 1), abortp, errp, PD_ERR_V_FULL)) return false;
+        tc_fence_after();
+        const uint32_t v0 = smem_u32(kv_s + s * 2 * PD_HALF + PD_HALF), p0 = smem_u32(p_s + pb * N * 128);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)                                // 32 tokens each
+          mma_e4m3(tmem + 2 * N + pb * N, smem_desc_sw128(v0 + k * 4096, PD_HALF, 1024),
+                   smem_desc_sw128(p0 + k * 32, 16, 1024), ID_O, k > 0 ? 1u : 0u);
+        mma_commit(&bars.o_full[pb]);
+        mma_commit(&bars.empty[s]);
+        return true;
+      };
+      while (ok && walk.next(sh, seq_len)) {
+        if (!mbar_wait(&bars.q_full, (uint32_t)(seg & 1), abortp, errp, PD_ERR_Q_FULL)) break;
+        ++seg;
+        for (int i = 0; i < walk.len; ++i, ++it) {
+          const int s = it % PD_STAGES;
+          if (!mbar_wait(&bars.k_full[s], (uint32_t)((it / PD_STAGES) & 1), abortp, errp, PD_ERR_K_FULL)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t k0 = smem_u32(kv_s + s * 2 * PD_HALF);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)                              // 32 dims each
+            mma_e4m3(tmem + (it & 1) * N, smem_desc_sw128(k0 + k * 32, 16, 1024), smem_desc_sw128(q0 + k * 32, 16, 1024),
+                     ID_S, k > 0 ? 1u : 0u);
+          mma_commit(&bars.s_full[it & 1]);
+          if (i > 0 && !issue_pv(it - 1)) { ok = false; break; }
+        }
+        if (ok && !issue_pv(it - 1)) ok = false;
+      }
+      mma_commit(&bars.final_bar);
+      mbar_wait_done(&bars.final_bar, 0, errp, PD_ERR_FINAL);   // also after an abort: the products finish on their own
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const int pg = tid >> sh.page_log2;                   // this thread's page of a tile
+    int it = 0;
+    bool ok = true, w = true;
+    // sequences without a visible token, spread over the CTAs
+    for (int b = blockIdx.x; b < sh.B; b += gridDim.x)
+      if (pd_tiles(sh, seq_len, b) == 0) {
+        for (int h = 0; h < sh.H; ++h) out[((size_t)b * sh.H + h) * kD + tid] = 0;
+        if (lse != nullptr && tid < sh.H) lse[(size_t)b * sh.H + tid] = -INFINITY;
+      }
+    if (tid == 0) {
+      int* h = ws.hdr + 8 * blockIdx.x;
+      h[0] = -1;
+      h[4] = (int)(per & 0xffffffff);
+      h[5] = (int)(per >> 32);
+    }
+    auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
+      bool y = true;
+      if (lane == 0) y = mbar_wait(bar, parity, abortp, errp, code);
+      if (!__shfl_sync(0xffffffffu, (int)y, 0)) w = false;
+    };
+    auto load_cols = [&](uint32_t col, float (&x)[N]) {
+#pragma unroll
+      for (int c = 0; c < N; c += 16) {
+        uint32_t r[16];
+        tmem_ld16(tmem + lane_off + col + c, r);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[c + i] = __uint_as_float(r[i]);
+      }
+    };
+    bool first_seg = true;
+    while (ok && walk.next(sh, seq_len)) {
+      const int b = walk.b, hk = walk.u / sh.HG, g0 = (walk.u - hk * sh.HG) * GP;
+      const int gc = min(GP, sh.G - g0);
+      const size_t row0 = (size_t)b * sh.H + hk * sh.G + g0;
+      int lo, t0;
+      const int n = pd_range(sh, seq_len, b, lo, t0);
+      // ---- q in two parts; every product with the last segment's q has completed
+      for (int g = warp; g < GP; g += 4) {
+        uint2 v = make_uint2(0u, 0u);
+        if (g < gc) v = reinterpret_cast<const uint2*>(q + (long long)b * sh.q_stride + (long long)(hk * sh.G + g0 + g) * kD)[lane];
+        const float f[4] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+        float am = 0.f;
+        bool fin = true;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = fabsf(f[i]);
+          fin = fin && a <= 3.402823466e38f;
+          am = fmaxf(am, a <= 3.402823466e38f ? a : 0.f);
+        }
+        am = warp_redux_max(am);
+        fin = __all_sync(0xffffffffu, fin);
+        // am in [2^e, 2^(e+1)): times 2^(7 - e); the exponent is held where both powers are normal
+        const int e = max(-110, (int)(__float_as_uint(am) >> 23) - 127) - 7;
+        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+        uint32_t hi = 0u, lw = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float a = f[i] * inv, c = f[i + 1] * inv;
+          const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(a, c), __NV_SATFINITE, __NV_E4M3);
+          const float2 d = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2, __NV_E4M3)));
+          const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2((a - d.x) * 16.f, (c - d.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
+          hi |= h2 << (8 * i);
+          lw |= l2 << (8 * i);
+        }
+        *reinterpret_cast<uint32_t*>(q_s + sw128(g, lane >> 2) + (lane & 3) * 4) = hi;
+        *reinterpret_cast<uint32_t*>(q_s + sw128(GP + g, lane >> 2) + (lane & 3) * 4) = lw;
+        // a row of q that is not finite has no finite score
+        if (lane == 0) sm->qs[g] = fin ? sh.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) : __int_as_float(0x7fc00000);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.q_full);
+      named_bar(1, 128);
+      float qs[GP], o[GP], l[GP], R[GP], r_prev[GP], p_prev[GP];
+#pragma unroll
+      for (int g = 0; g < GP; ++g) { qs[g] = sm->qs[g]; o[g] = 0.f; l[g] = 0.f; R[g] = -INFINITY; r_prev[g] = 0.f; p_prev[g] = 0.f; }
+      // tile j's O^T and probabilities join the sums
+      auto join = [&](int j) {
+        wait(&bars.o_full[j & 1], (uint32_t)((j >> 1) & 1), PD_ERR_O_FULL);
+        tc_fence_after();
+        float x[N];
+        load_cols(2 * N + (j & 1) * N, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+          // a tile without a score (reference -inf) adds zeros, one of NaN scores its NaN
+          const float Rn = fmaxf(R[g], r_prev[g]);
+          const float a = R[g] == Rn ? 1.f : ex2_approx(R[g] - Rn);
+          const float f = r_prev[g] > -INFINITY && r_prev[g] != Rn ? ex2_approx(r_prev[g] - Rn) : 1.f;
+          o[g] = fmaf(f, fmaf(x[GP + g], 0.0625f, x[g]), o[g] * a);
+          l[g] = fmaf(f, p_prev[g], l[g] * a);
+          R[g] = Rn;
+        }
+      };
+      for (int i = 0; i < walk.len; ++i, ++it) {
+        const int s = it % PD_STAGES, sb = it & 1;
+        const int tok = (t0 + walk.t + i) * PD_TILE + tid;
+        wait(&bars.k_full[s], (uint32_t)((it / PD_STAGES) & 1), PD_ERR_K_FULL);   // the page's scales are there
+        wait(&bars.s_full[sb], (uint32_t)((it >> 1) & 1), PD_ERR_S_FULL);
+        __syncwarp();
+        tc_fence_after();
+        float x[N], p[GP];
+        load_cols(sb * N, x);
+        const float ks = sm->ks[s][pg];
+        const int ev = sm->ev[s][pg];
+        const bool seen = tok >= lo && tok < n && ev != PD_ABSENT;
+        const float evf = (float)ev;
+        tmem_wait_ld();
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+          const float sc = fmaf(x[GP + g], 0.0625f, x[g]) * ks;
+          p[g] = seen ? fmaf(sc, qs[g], evf) : -INFINITY;
+          const float mx = warp_redux_max(p[g]);
+          if (lane == 0) sm->smax[sb][g][warp] = mx;
+        }
+        // all scores are read: one vote on the waits, which also publishes the maxima
+        ok = !named_bar_or(1, 128, !w || *abortp != 0);
+        if (!ok) break;
+        const float einv = seen ? __uint_as_float((uint32_t)(127 - ev) << 23) : 0.f;
+        uint8_t* pt = p_s + sb * N * 128;
+        float r_now[GP];
+#pragma unroll
+        for (int g = 0; g < GP; g += 2) {
+          float pr[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float4 m4 = *reinterpret_cast<const float4*>(sm->smax[sb][g + k]);
+            const float mx = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+            r_now[g + k] = mx - 8.f;                       // the tile's largest probability becomes 2^8
+            pr[k] = ex2_approx(p[g + k] - (mx == -INFINITY ? 0.f : r_now[g + k]));
+            p[g + k] = pr[k] * einv;
+          }
+          const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(pr[0], pr[1]), __NV_SATFINITE, __NV_E4M3);
+          const float2 d = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2, __NV_E4M3)));
+          const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2((pr[0] - d.x) * 16.f, (pr[1] - d.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
+          const int ck = tid >> 4, by = tid & 15;
+          pt[sw128(g, ck) + by] = (uint8_t)h2;
+          pt[sw128(g + 1, ck) + by] = (uint8_t)(h2 >> 8);
+          pt[sw128(GP + g, ck) + by] = (uint8_t)l2;
+          pt[sw128(GP + g + 1, ck) + by] = (uint8_t)(l2 >> 8);
+        }
+        // a tile with tokens that are not seen: their stale V rows may hold NaN
+        const int first = (t0 + walk.t + i) * PD_TILE;
+        if (first < lo || first + PD_TILE > n) {
+          wait(&bars.v_full[s], (uint32_t)((it / PD_STAGES) & 1), PD_ERR_V_FULL);
+          __syncwarp();
+          if (w && !seen) {
+            uint4* row = reinterpret_cast<uint4*>(kv_s + s * 2 * PD_HALF + PD_HALF + tid * 128);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) row[c] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[sb]);
+        if (i > 0) join(it - 1);
+#pragma unroll
+        for (int g = 0; g < GP; ++g) { r_prev[g] = r_now[g]; p_prev[g] = p[g]; }
+      }
+      if (!ok) break;
+      join(it - 1);
+      // ---- the segment's sums
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        const float t = warp_sum(l[g]);
+        if (lane == 0) sm->lsum[g][warp] = t;
+      }
+      tc_fence_before();
+      ok = !named_bar_or(1, 128, !w || *abortp != 0);
+      if (!ok) break;
+      const bool whole = walk.len == walk.nt;
+      const int slot = 2 * blockIdx.x + (first_seg ? 0 : 1);
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        const float lt = (sm->lsum[g][0] + sm->lsum[g][1]) + (sm->lsum[g][2] + sm->lsum[g][3]);
+        if (whole) {
+          if (g < gc) {
+            const float inv = lt == 0.f ? 0.f : 1.f / lt;
+            out[(row0 + g) * kD + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(o[g] * inv));
+            if (lse != nullptr && tid == 0) lse[row0 + g] = lt == 0.f ? -INFINITY : (R[g] + log2f(lt)) * kLn2;
+          }
+        } else {
+          ws.o[((size_t)slot * GP + g) * kD + tid] = o[g];
+          if (tid == 0) ws.rl[(size_t)slot * GP + g] = make_float2(R[g], lt);
+        }
+      }
+      if (first_seg && walk.t > 0 && tid == 0) {
+        int* h = ws.hdr + 8 * blockIdx.x;
+        h[0] = b; h[1] = walk.u; h[2] = walk.t; h[3] = walk.nt;
+      }
+      first_seg = false;
+      named_bar(1, 128);                                   // lsum and qs are free again
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  tc_fence_before();
+  __syncthreads();
+  if (warp == PD_MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 4 * N < 32 ? 32 : 4 * N);
+  }
+}
+
+// CTA c merges the unit that crosses from CTA c - 1 into CTA c, if c is the
+// first border inside it. Thread = dim.
+template <int GP>
+__global__ void __launch_bounds__(128) page_decode_combine_kernel(PdShape sh, PdWs ws, uint16_t* __restrict__ out,
+                                                                  float* __restrict__ lse) {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int c = blockIdx.x + 1, tid = threadIdx.x;
+  const int* h = ws.hdr + 8 * c;
+  const int b = h[0];
+  if (b < 0) return;
+  const long long per = ((long long)h[5] << 32) | (uint32_t)h[4];
+  const int u = h[1];
+  const long long a = per * c - h[2], e = a + h[3];        // the unit's tiles
+  const int c0 = (int)(a / per), c1 = (int)((e - 1) / per);
+  if (c0 != c - 1) return;
+  const int hk = u / sh.HG, g0 = (u - hk * sh.HG) * GP, gc = min(GP, sh.G - g0);
+  const int s0 = a == per * c0 ? 2 * c0 : 2 * c0 + 1;
+  for (int g = blockIdx.y; g < gc; g += gridDim.y) {
+    auto slot = [&](int k) { return k == c0 ? s0 : 2 * k; };
+    float R = -INFINITY;
+    for (int k = c0; k <= c1; ++k) R = fmaxf(R, ws.rl[(size_t)slot(k) * GP + g].x);
+    float l = 0.f, o = 0.f;
+    for (int k = c0; k <= c1; ++k) {
+      const float2 rl = ws.rl[(size_t)slot(k) * GP + g];
+      const float f = rl.x > -INFINITY && rl.x != R ? ex2_approx(rl.x - R) : 1.f;   // -inf: zeros, or NaN scores
+      l = fmaf(rl.y, f, l);
+      o = fmaf(ws.o[((size_t)slot(k) * GP + g) * kD + tid], f, o);
+    }
+    const size_t row = (size_t)b * sh.H + hk * sh.G + g0 + g;
+    out[row * kD + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(o * (l == 0.f ? 0.f : 1.f / l)));
+    if (lse != nullptr && tid == 0) lse[row] = l == 0.f ? -INFINITY : (R + log2f(l)) * kLn2;
+  }
+}
+
+namespace {
+
+// Query heads of one unit. Groups of up to 8 heads fill N = 16 columns; larger
+// groups take 16 heads at a time (N = 32) and read the cache once for each 16.
+int pd_group(int G) { return G <= 8 ? 8 : 16; }
+
+template <int GP>
+constexpr size_t pd_smem() {
+  return 1024 + (size_t)PD_STAGES * 2 * PD_HALF + 3 * 2 * GP * 128 + sizeof(PdSmall<GP>);
+}
+
+template <int GP>
+cslc_status pd_launch(const PdShape& sh, const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                      const float* k_scale, const float* v_scale, const int32_t* table, const int32_t* seq_len,
+                      uint16_t* out, float* lse, uint8_t* wsp, cudaStream_t stream) {
+  cudaError_t err = cudaFuncSetAttribute(page_decode_sm100_kernel<GP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)pd_smem<GP>());
+  if (err != cudaSuccess) return set_error(CSLC_ERR_CUDA, "cslc_page_decode_attn: %s", cudaGetErrorString(err));
+  // an empty cache has no page to load; its map only has to be valid
+  const uint64_t rows = (uint64_t)sh.n_pages * sh.Hkv << sh.page_log2;
+  const void* kb = rows ? (const void*)k_cache : (const void*)q;
+  const void* vb = rows ? (const void*)v_cache : (const void*)q;
+  CUtensorMap tm_k, tm_v;
+  if (!make_tmap_u8_rows128(&tm_k, kb, rows ? rows : 1, 1u << sh.page_log2) ||
+      !make_tmap_u8_rows128(&tm_v, vb, rows ? rows : 1, 1u << sh.page_log2))
+    return set_error(CSLC_ERR_CUDA, "cslc_page_decode_attn: tensor map encoding failed");
+  PdWs ws;
+  ws.hdr = reinterpret_cast<int*>(wsp);
+  ws.rl = reinterpret_cast<float2*>(wsp + PD_CTAS * 32);
+  ws.o = reinterpret_cast<float*>(wsp + PD_CTAS * 32 + (size_t)2 * PD_CTAS * GP * sizeof(float2));
+  const long long most = (long long)sh.B * sh.Hkv * sh.HG *
+                         ((((long long)sh.max_pages << sh.page_log2) + PD_TILE - 1) / PD_TILE);
+  const int grid = (int)(most < 1 ? 1 : most < PD_CTAS ? most : PD_CTAS);
+  page_decode_sm100_kernel<GP><<<grid, PD_THREADS, pd_smem<GP>(), stream>>>(sh, q, k_scale, v_scale, table, seq_len, out,
+                                                                           lse, ws, tm_k, tm_v);
+  cslc_status st = check_launch("page_decode_sm100_kernel");
+  if (st != CSLC_OK || grid == 1) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid - 1, sh.G < GP ? sh.G : GP);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, page_decode_combine_kernel<GP>, sh, ws, out, lse);
+  if (err != cudaSuccess) return set_error(CSLC_ERR_CUDA, "page_decode_combine_kernel: %s", cudaGetErrorString(err));
+  return CSLC_OK;
+}
+
+}  // namespace
+
+size_t page_decode_workspace_bytes(int, int H, int Hkv) {
+  const int GP = pd_group(H / Hkv);
+  return PD_CTAS * 32 + (size_t)2 * PD_CTAS * GP * (sizeof(float2) + kD * sizeof(float));
+}
+
+cslc_status launch_page_decode(const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
+                               const float* v_scale, const int32_t* table, const int32_t* seq_len, int B, int H,
+                               int Hkv, int page, int n_pages, int max_pages, long long q_stride, int window,
+                               float scale, uint16_t* out, float* lse, void* ws, cudaStream_t stream) {
+  const int G = H / Hkv, GP = pd_group(G);
+  const PdShape sh{B, H, Hkv, G, (G + GP - 1) / GP, 31 - __builtin_clz(page), n_pages, max_pages, window, scale * kLog2e, q_stride};
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  return GP == 8 ? pd_launch<8>(sh, q, k_cache, v_cache, k_scale, v_scale, table, seq_len, out, lse, w, stream)
+                 : pd_launch<16>(sh, q, k_cache, v_cache, k_scale, v_scale, table, seq_len, out, lse, w, stream);
+}
+
+int page_decode_sm100_read_error() {
+  int v = 0, zero = 0;
+  cudaMemcpyFromSymbol(&v, g_page_decode_err, sizeof(int));
+  if (v) cudaMemcpyToSymbol(g_page_decode_err, &zero, sizeof(int));
+  return v;
+}
+
+CSLC_DEFINE_WAIT_LIMIT_SETTER(page_decode_sm100_set_wait_limits)
+
+}  // namespace cslc

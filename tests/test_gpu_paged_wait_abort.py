@@ -1,0 +1,51 @@
+"""The bounded-wait failure path of the paged attention kernels: with the wait
+limit at 0 ns the first wait that is not satisfied gives up, the status says so,
+and the same call then runs normally (see test_gpu_wait_abort.py)."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_oracle as PO
+from tests import test_gpu_paged as TP
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def C(cuda_device):
+    from compressed_sparse_long_compress_b200 import cslc
+    return cslc
+
+
+@pytest.fixture(autouse=True)
+def _restore_limits(cuda_device):
+    yield
+    from compressed_sparse_long_compress_b200 import cslc
+    cslc.testing_set_wait_limits(cslc.WAIT_LIMIT_NS_DEFAULT, cslc.WAIT_SLEEP_NS_DEFAULT)
+
+
+def _aborts(C, run, name):
+    C.testing_set_wait_limits(0, 0)
+    run()
+    with pytest.raises(C.CslcError) as ei:
+        C.sync_status()
+    assert ei.value.status == 7 and "timed out" in str(ei.value) and name in str(ei.value)
+    C.testing_set_wait_limits(C.WAIT_LIMIT_NS_DEFAULT, C.WAIT_SLEEP_NS_DEFAULT)
+
+
+@pytest.mark.parametrize("H", [8, 16])
+def test_decode_wait_abort_then_recovers(C, H):
+    cache = TP.make_cache(700, 1, 64, 5)
+    table = TP.i32(np.random.RandomState(3).randint(0, 700, (6, 100)))
+    lens = [6400, 3000, 1, 0, 5000, 777]
+    q, n = TP.randn((6, H, 128), 8), TP.i32(lens)
+    run = lambda: C.page_decode_attn(q, *cache, table, n, TP.SCALE, lse=True)  # noqa: E731
+    _aborts(C, run, "cslc_page_decode_attn")
+    out, lse = run()
+    C.sync_status()
+    kc, vc, ks, vs = (x.cpu().numpy() for x in cache)
+    ref = PO.page_decode_attention(TP.f64(q), kc, vc, ks.astype(float), vs.astype(float), table.cpu().numpy(), lens, TP.SCALE)
+    TP.check_attention(out, lse, ref, max(lens), "decode after an abort")
