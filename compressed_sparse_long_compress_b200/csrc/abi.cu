@@ -48,11 +48,13 @@ int dense_attn_sm100_read_error();
 int indexer_sm100_read_error();
 int front_end_sm100_read_error();
 int page_decode_sm100_read_error();
+int prompt_attn_sm100_read_error();
 cudaError_t sparse_attn_sm100_set_wait_limits(uint64_t, uint32_t);
 cudaError_t dense_attn_sm100_set_wait_limits(uint64_t, uint32_t);
 cudaError_t indexer_sm100_set_wait_limits(uint64_t, uint32_t);
 cudaError_t front_end_sm100_set_wait_limits(uint64_t, uint32_t);
 cudaError_t page_decode_sm100_set_wait_limits(uint64_t, uint32_t);
+cudaError_t prompt_attn_sm100_set_wait_limits(uint64_t, uint32_t);
 cslc_status launch_front_end(const uint16_t*, const uint16_t*, const uint16_t*, int, int, int, int, int, uint16_t*,
                              cudaStream_t);
 size_t decode_topk_workspace_bytes(int, int, int);
@@ -161,6 +163,9 @@ cslc_status cslc_sync_status(cslc_stream_t stream) {
   const int code5 = page_decode_sm100_read_error();
   if (code5 != 0)
     return set_error(CSLC_ERR_DEVICE_CHECK, "cslc_page_decode_attn: a pipeline wait timed out (code %d)", code5);
+  const int code6 = prompt_attn_sm100_read_error();
+  if (code6 != 0)
+    return set_error(CSLC_ERR_DEVICE_CHECK, "cslc_prompt_attn: a pipeline wait timed out (code %d)", code6);
   return CSLC_OK;
 }
 
@@ -170,6 +175,7 @@ cslc_status cslc_testing_set_wait_limits(uint64_t limit_ns, uint32_t sleep_ns) {
   if (e == cudaSuccess) e = indexer_sm100_set_wait_limits(limit_ns, sleep_ns);
   if (e == cudaSuccess) e = front_end_sm100_set_wait_limits(limit_ns, sleep_ns);
   if (e == cudaSuccess) e = page_decode_sm100_set_wait_limits(limit_ns, sleep_ns);
+  if (e == cudaSuccess) e = prompt_attn_sm100_set_wait_limits(limit_ns, sleep_ns);
   if (e != cudaSuccess) return set_error(CSLC_ERR_CUDA, "cslc_testing_set_wait_limits: %s", cudaGetErrorString(e));
   return CSLC_OK;
 }
@@ -591,6 +597,7 @@ cslc_status cslc_prompt_attn(const cslc_bf16* q, const cslc_bf16* k, const cslc_
   FORWARD(check_stride(fn, "q_stride", q_stride, H));
   FORWARD(check_stride(fn, "k_stride", k_stride, Hkv));
   FORWARD(check_stride(fn, "v_stride", v_stride, Hkv));
+  REQUIRE(scale > 0.f && scale <= 3.402823466e38f, CSLC_ERR_UNSUPPORTED, "%s: scale must be positive and finite", fn);
   REQUIRE((long long)Tq * H < (1ll << 31) && (long long)Tk * Hkv < (1ll << 31), CSLC_ERR_UNSUPPORTED,
           "%s: Tq * H and Tk * H_kv must be below 2^31", fn);
   if (B == 0 || Tq == 0) return CSLC_OK;
@@ -621,6 +628,7 @@ cslc_status cslc_page_decode_attn(const cslc_bf16* q, const uint8_t* k_cache, co
   FORWARD(check_heads(fn, H, Hkv, D));
   FORWARD(check_pages(fn, Hkv, page, n_pages));
   FORWARD(check_stride(fn, "q_stride", q_stride, H));
+  REQUIRE(scale > 0.f && scale <= 3.402823466e38f, CSLC_ERR_UNSUPPORTED, "%s: scale must be positive and finite", fn);
   if (B == 0) return CSLC_OK;
   REQUIRE_PTR(q); REQUIRE_PTR(seq_len); REQUIRE_PTR(out);
   if (max_pages > 0) REQUIRE_PTR(block_table);

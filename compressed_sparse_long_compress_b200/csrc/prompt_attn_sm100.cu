@@ -1,0 +1,714 @@
+// Causal attention of packed sequences with grouped heads, on the 5th-generation
+// tensor cores (tcgen05 + TMEM).
+//
+// Rows of a product are (token, head of the key head's group) pairs: with G
+// heads to a key head a Q tile holds floor(128 / G) tokens. An item is two
+// consecutive Q tiles of one sequence and key head; their keys and values are
+// read once for both. Query i of a sequence sees the keys
+// max(0, i + off - window + 1) .. i + off, off = nk - nq.
+//
+// CTA roles (persistent, one CTA per SM):
+//   warps 0-3, 4-7  softmax and epilogue of Q tile 0 and 1, thread = row = TMEM
+//                   lane. The row's reference m is the exact maximum of its
+//                   first visible tile and moves only when a tile's
+//                   probabilities sum above 2^64 (O in TMEM is rescaled then),
+//                   so the steady state needs no maximum. P goes back to TMEM
+//                   as bf16 over the tile's own scores and is the A operand of
+//                   P V from there: no shared memory and no proxy fence.
+//   warp 8          producer: Q tiles, K and V tiles (TMA, 5-deep ring of 32 KB)
+//   warp 9          TMEM allocation and the MMA-issuing thread. Order of issue:
+//                   PV0(j-1) S0(j) PV1(j-1) S1(j): while one tile's softmax
+//                   runs, the products of the other fill the tensor pipe. S_w(j)
+//                   overwrites P_w(j-1), which the PV issued just before it
+//                   reads: products of one thread run in the order of issue.
+// TMEM: S0 S1 (P over them) O0 O1, 128 columns each.
+//
+// Order of work. prompt_schedule_kernel sorts the Q-tile pairs of all sequences
+// by their number of key tiles, largest first; the CTAs draw tickets, so ragged
+// and causal work evens out. The pairs of one key head are drawn together, so
+// that its keys and values stay in L2. Few items (at most one for each CTA)
+// need no order and no ticket.
+//
+// A value that is masked for some row of a tile may be NaN or infinite, and
+// 0 * NaN would reach that row through the product. So the V tiles that are
+// masked in part (about two for each Q tile) are scanned, and where one is not
+// finite its P V is done on the CUDA cores, without the masked entries.
+// All waits are time-bounded; no barrier without a bound is used in the loop.
+
+#include "sm100.cuh"
+
+namespace cslc {
+
+using namespace sm100;
+
+__device__ int g_prompt_attn_err = 0;
+
+namespace {
+
+constexpr int PA_THREADS = 320;
+constexpr int PA_PROD_WARP = 8;
+constexpr int PA_MMA_WARP = 9;
+constexpr int PA_TILE = 128;
+constexpr int PA_SLOTS = 5;
+constexpr int PA_TILE_BYTES = PA_TILE * 256;     // 32 KB: a Q, K or V tile
+constexpr float PA_SUM_MAX = 1.8446744e19f;      // 2^64
+constexpr int PA_BUCKETS = 512;
+constexpr int PA_SCHED_THREADS = 1024;
+
+enum { PA_ERR_ITEM = 1, PA_ERR_Q_EMPTY, PA_ERR_EMPTY, PA_ERR_Q_FULL, PA_ERR_K_FULL, PA_ERR_V_FULL, PA_ERR_P_FULL,
+       PA_ERR_O_FREE, PA_ERR_S_FULL, PA_ERR_PV_DONE, PA_ERR_SCAN, PA_ERR_FINAL };
+
+struct __align__(8) PaBars {
+  uint64_t full[PA_SLOTS], empty[PA_SLOTS];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2], scan[2];
+  uint64_t item_full[2], item_empty[2];
+  uint64_t final_bar;
+};
+
+struct PaSmall {
+  PaBars bars;
+  int4 item[2];                                  // b, pair, key head; b = -1: no more
+  int bad_v[2][2];                               // [Q tile][parity]: the scanned V tile is not finite
+  int skip[2];                                   // [Q tile]: this P V is not the tensor cores'
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+struct PaShape {
+  int B, Tq, Tk, H, Hkv, G, tpt, window;
+  float scale, scale_log2;
+  int direct;                                    // no schedule: CTA = item
+};
+
+// One item: two Q tiles of sequence b at its tokens t0 .. t0 + 2 tpt - 1.
+struct PaItem {
+  int q0, nq, k0, off, t0;                       // rows of q and k, nk - nq, first token
+  int n[2], s[2], e[2];                          // per Q tile: tokens, key tiles [s, e)
+  int jb, je;
+};
+
+__device__ __forceinline__ void pa_seq(const PaShape& sh, const int32_t* __restrict__ cu_q,
+                                       const int32_t* __restrict__ cu_k, int b, int& q0, int& nq, int& k0, int& nk) {
+  q0 = min(max(cu_q[b], 0), sh.Tq);
+  nq = min(max(cu_q[b + 1], q0), sh.Tq) - q0;
+  k0 = min(max(cu_k[b], 0), sh.Tk);
+  nk = min(max(cu_k[b + 1], k0), sh.Tk) - k0;
+}
+
+__device__ __forceinline__ PaItem pa_item(const PaShape& sh, const int32_t* __restrict__ cu_q,
+                                          const int32_t* __restrict__ cu_k, int b, int pair) {
+  PaItem it;
+  int nk;
+  pa_seq(sh, cu_q, cu_k, b, it.q0, it.nq, it.k0, nk);
+  it.off = nk - it.nq;
+  it.t0 = pair * 2 * sh.tpt;
+  it.jb = 0x7fffffff;
+  it.je = 0;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int tw = it.t0 + w * sh.tpt;
+    it.n[w] = min(max(it.nq - tw, 0), sh.tpt);
+    it.s[w] = it.e[w] = 0;
+    const int last = tw + it.n[w] - 1 + it.off;  // the last token's last key
+    if (it.n[w] > 0 && last >= 0) {
+      it.e[w] = last / PA_TILE + 1;
+      it.s[w] = sh.window > 0 ? max(0, tw + it.off - sh.window + 1) / PA_TILE : 0;
+      it.jb = min(it.jb, it.s[w]);
+      it.je = max(it.je, it.e[w]);
+    }
+  }
+  if (it.je == 0) it.jb = 0;
+  return it;
+}
+
+__device__ __forceinline__ int pa_pairs(const PaShape& sh, int nq) { return (nq + 2 * sh.tpt - 1) / (2 * sh.tpt); }
+
+// D[tmem] (+)= A[tmem] * B[smem]^T (kind::f16, K = 16): bf16 A, two values to a column.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n" : "=r"(r) : "r"(taddr));
+  return r;
+}
+
+}  // namespace
+
+// The workspace: tickets drawn, number of pairs (16 bytes), then the pairs (b, index) in the order of work.
+struct PaWs {
+  int* head;
+  int2* list;
+  int cap;                                       // entries of the list
+};
+
+// One CTA: pairs of all sequences, counting sort by their key tiles, largest first.
+__global__ void __launch_bounds__(PA_SCHED_THREADS) prompt_schedule_kernel(PaShape sh, const int32_t* __restrict__ cu_q,
+                                                                           const int32_t* __restrict__ cu_k, PaWs ws) {
+  extern __shared__ int pa_before[];             // [B + 1] pairs before sequence b
+  __shared__ int warp_sum_s[PA_SCHED_THREADS / 32];
+  __shared__ int bucket[PA_BUCKETS];
+  __shared__ int most_s;
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");   // the attention's CTAs set up meanwhile
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int each = (sh.B + PA_SCHED_THREADS - 1) / PA_SCHED_THREADS;
+  const int b0 = min(sh.B, tid * each), b1 = min(sh.B, b0 + each);
+  int sum = 0, most = 0;
+  for (int b = b0; b < b1; ++b) {
+    int q0, nq, k0, nk;
+    pa_seq(sh, cu_q, cu_k, b, q0, nq, k0, nk);
+    sum += pa_pairs(sh, nq);
+    most = max(most, (nk + PA_TILE - 1) / PA_TILE);
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_sum_s[warp] = incl;
+  if (tid == 0) most_s = 0;
+  for (int i = tid; i < PA_BUCKETS; i += PA_SCHED_THREADS) bucket[i] = 0;
+  __syncthreads();
+  atomicMax(&most_s, most);
+  for (int w = 0; w < warp; ++w) incl += warp_sum_s[w];
+  int at = incl - sum;
+  for (int b = b0; b < b1; ++b) {
+    pa_before[b] = at;
+    int q0, nq, k0, nk;
+    pa_seq(sh, cu_q, cu_k, b, q0, nq, k0, nk);
+    at += pa_pairs(sh, nq);
+  }
+  if (b0 < sh.B && b1 == sh.B) pa_before[sh.B] = at;
+  __syncthreads();
+  const int n = min(pa_before[sh.B], ws.cap);     // more only where cu_q is not ascending
+  // bucket 0: the most key tiles (with a window never more than the window and a pair's tokens span)
+  int top = most_s;
+  if (sh.window > 0) top = min(top, (sh.window + 2 * sh.tpt) / PA_TILE + 2);
+  auto pair_of = [&](int i, int& b, int& pair) {
+    int lo = 0, hi = sh.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pa_before[mid] <= i) lo = mid; else hi = mid;
+    }
+    b = lo;
+    pair = i - pa_before[lo];
+    const PaItem it = pa_item(sh, cu_q, cu_k, b, pair);
+    return (int)((long long)max(0, top - (it.je - it.jb)) * (PA_BUCKETS - 1) / max(1, top));
+  };
+  for (int i = tid; i < n; i += PA_SCHED_THREADS) {
+    int b, pair;
+    atomicAdd(&bucket[pair_of(i, b, pair)], 1);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int c[PA_BUCKETS / 32], s = 0;
+#pragma unroll
+    for (int k = 0; k < PA_BUCKETS / 32; ++k) { c[k] = bucket[lane * (PA_BUCKETS / 32) + k]; s += c[k]; }
+    int in = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, in, o);
+      if (lane >= o) in += y;
+    }
+    in -= s;
+#pragma unroll
+    for (int k = 0; k < PA_BUCKETS / 32; ++k) { bucket[lane * (PA_BUCKETS / 32) + k] = in; in += c[k]; }
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += PA_SCHED_THREADS) {
+    int b, pair;
+    const int k = pair_of(i, b, pair);
+    ws.list[atomicAdd(&bucket[k], 1)] = make_int2(b, pair);
+  }
+  if (tid == 0) { ws.head[0] = 0; ws.head[1] = n; }
+}
+
+__global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
+    PaShape sh, const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, PaWs ws, uint16_t* __restrict__ out,
+    float* __restrict__ lse, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+    const __grid_constant__ CUtensorMap tm_v) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* q_s = smem;                                   // [2 tiles][2 halves][128][128 B]
+  uint8_t* ring = q_s + 2 * PA_TILE_BYTES;               // [SLOTS][2 halves][128][128 B]
+  PaSmall* sm = reinterpret_cast<PaSmall*>(ring + PA_SLOTS * PA_TILE_BYTES);
+  PaBars& bars = sm->bars;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rows = sh.tpt * sh.G;                        // rows of a Q tile that hold a (token, head)
+
+  if (tid == 0) {
+    for (int s = 0; s < PA_SLOTS; ++s) { mbar_init(&bars.full[s], 1); mbar_init(&bars.empty[s], 1); }
+    mbar_init(&bars.q_full, 1); mbar_init(&bars.q_empty, 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&bars.s_full[w], 1); mbar_init(&bars.p_full[w], 4); mbar_init(&bars.pv_done[w], 1);
+      mbar_init(&bars.o_free[w], 4); mbar_init(&bars.scan[w], 4);
+      mbar_init(&bars.item_full[w], 1); mbar_init(&bars.item_empty[w], 9);
+      sm->skip[w] = 0;
+      sm->bad_v[w][0] = sm->bad_v[w][1] = 0;
+    }
+    mbar_init(&bars.final_bar, 1);
+    sm->abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == PA_MMA_WARP) tmem_alloc(&sm->tmem_base, 512);
+  // rows of no (token, head) are never loaded: zeros, so that their scores are finite
+  if (rows < PA_TILE)
+    for (int i = tid; i < 4 * (PA_TILE - rows) * 8; i += PA_THREADS) {
+      const int part = i / ((PA_TILE - rows) * 8), r = i % ((PA_TILE - rows) * 8);
+      reinterpret_cast<uint4*>(q_s + part * (PA_TILE * 128) + rows * 128)[r] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the schedule
+  const uint32_t tmem = sm->tmem_base;
+  volatile int* abortp = &sm->abort_flag;
+  int* errp = &g_prompt_attn_err;
+
+  // the item in slot n & 1 of the hand-over, read by every role; false: no more, or a wait gave up
+  auto take_item = [&](int n, int4& x) -> bool {
+    bool ok = true;
+    if (lane == 0) ok = mbar_wait(&bars.item_full[n & 1], (uint32_t)((n >> 1) & 1), abortp, errp, PA_ERR_ITEM);
+    if (__shfl_sync(0xffffffffu, (int)ok, 0) == 0) return false;
+    x = sm->item[n & 1];
+    return x.x >= 0;
+  };
+
+  if (warp == PA_PROD_WARP) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_map(&tm_q); tma_prefetch_map(&tm_k); tma_prefetch_map(&tm_v);
+      int kv = 0;                                        // tiles put into the ring
+      int n = 0, q_loads = 0;
+      bool ok = true;
+      auto load_tile = [&](const CUtensorMap* map, int hk, int row) -> bool {
+        const int s = kv % PA_SLOTS;
+        if (kv >= PA_SLOTS &&
+            !mbar_wait(&bars.empty[s], (uint32_t)((kv / PA_SLOTS - 1) & 1), abortp, errp, PA_ERR_EMPTY))
+          return false;
+        uint8_t* dst = ring + s * PA_TILE_BYTES;
+        mbar_arrive_expect_tx(&bars.full[s], PA_TILE_BYTES);
+        tma_load_3d(dst, map, 0, hk, row, &bars.full[s]);
+        tma_load_3d(dst + PA_TILE * 128, map, 64, hk, row, &bars.full[s]);
+        ++kv;
+        return true;
+      };
+      const int n_pairs = sh.direct ? 0 : ws.head[1];
+      const long long n_items = (long long)n_pairs * sh.Hkv;
+      for (;; ++n) {
+        int4 x = make_int4(-1, 0, 0, 0);
+        if (sh.direct) {
+          if (n == 0) {                                  // item = CTA: the pair by a walk over the sequences
+            int pair = blockIdx.x / sh.Hkv;
+            for (int b = 0; b < sh.B; ++b) {
+              int q0, nq, k0, nk;
+              pa_seq(sh, cu_q, cu_k, b, q0, nq, k0, nk);
+              const int p = pa_pairs(sh, nq);
+              if (pair < p) { x = make_int4(b, pair, blockIdx.x % sh.Hkv, 0); break; }
+              pair -= p;
+            }
+          }
+        } else {
+          const long long i = atomicAdd(ws.head, 1);
+          if (i < n_items) {
+            const int2 bp = ws.list[i % n_pairs];
+            x = make_int4(bp.x, bp.y, (int)(i / n_pairs), 0);
+          }
+        }
+        if (n >= 2 && !mbar_wait(&bars.item_empty[n & 1], (uint32_t)(((n >> 1) - 1) & 1), abortp, errp, PA_ERR_ITEM)) break;
+        sm->item[n & 1] = x;
+        mbar_arrive(&bars.item_full[n & 1]);
+        if (x.x < 0) break;
+        const PaItem it = pa_item(sh, cu_q, cu_k, x.x, x.y);
+        const int hk = x.z;
+        if (it.jb < it.je && !load_tile(&tm_k, hk, it.k0 + it.jb * PA_TILE)) break;
+        if (n >= 1 && !mbar_wait(&bars.q_empty, (uint32_t)((n - 1) & 1), abortp, errp, PA_ERR_Q_EMPTY)) break;
+        q_loads = n + 1;
+        mbar_arrive_expect_tx(&bars.q_full, (uint32_t)(4 * rows * 128));
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const int tok = it.q0 + it.t0 + w * sh.tpt;
+          tma_load_3d(q_s + w * PA_TILE_BYTES, &tm_q, 0, hk * sh.G, tok, &bars.q_full);
+          tma_load_3d(q_s + w * PA_TILE_BYTES + PA_TILE * 128, &tm_q, 64, hk * sh.G, tok, &bars.q_full);
+        }
+        for (int j = it.jb; j < it.je && ok; ++j) {
+          if (j > it.jb) ok = load_tile(&tm_k, hk, it.k0 + j * PA_TILE);
+          if (ok) ok = load_tile(&tm_v, hk, it.k0 + j * PA_TILE);
+        }
+        if (!ok) break;
+      }
+      // loads in flight after an abort land before the CTA leaves
+      if (q_loads > 0) mbar_wait_done(&bars.q_full, (uint32_t)((q_loads - 1) & 1), errp, PA_ERR_Q_FULL);
+      for (int d = 1; d <= PA_SLOTS && kv - d >= 0; ++d) {
+        const int k2 = kv - d;
+        mbar_wait_done(&bars.full[k2 % PA_SLOTS], (uint32_t)((k2 / PA_SLOTS) & 1), errp, PA_ERR_K_FULL);
+      }
+    }
+    __syncwarp();
+  } else if (warp == PA_MMA_WARP) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t ID_O = idesc_bf16(128, 128, false, true);
+      int kv0 = 0;                                       // ring position of the item's first K
+      int p_it[2] = {0, 0}, o_it[2] = {0, 0};            // P tiles taken, items with a tile
+      bool ok = true;
+      int4 x;
+      for (int n = 0; ok; ++n) {
+        if (!mbar_wait(&bars.item_full[n & 1], (uint32_t)((n >> 1) & 1), abortp, errp, PA_ERR_ITEM)) break;
+        x = sm->item[n & 1];
+        mbar_arrive(&bars.item_empty[n & 1]);
+        if (x.x < 0) break;
+        const PaItem it = pa_item(sh, cu_q, cu_k, x.x, x.y);
+        if (!mbar_wait(&bars.q_full, (uint32_t)(n & 1), abortp, errp, PA_ERR_Q_FULL)) break;
+        if (it.jb == it.je) { mma_commit(&bars.q_empty); continue; }
+        // ring position of K_j: kv0 + 2 (j - jb), of V_j the one behind it
+        for (int j = it.jb; j <= it.je && ok; ++j) {
+          const int kk = kv0 + 2 * (j - it.jb), vv = kk - 1;
+          const int ks = kk % PA_SLOTS, vs = j > it.jb ? vv % PA_SLOTS : 0;
+          bool k_there = false, v_there = false;
+          for (int w = 0; w < 2 && ok; ++w) {
+            if (j > it.s[w] && j <= it.e[w]) {           // P_w V of tile j - 1
+              if (!v_there) ok = mbar_wait(&bars.full[vs], (uint32_t)((vv / PA_SLOTS) & 1), abortp, errp, PA_ERR_V_FULL);
+              v_there = true;
+              const bool first = j - 1 == it.s[w];
+              if (ok && first && o_it[w] > 0)
+                ok = mbar_wait(&bars.o_free[w], (uint32_t)((o_it[w] - 1) & 1), abortp, errp, PA_ERR_O_FREE);
+              if (ok) ok = mbar_wait(&bars.p_full[w], (uint32_t)(p_it[w] & 1), abortp, errp, PA_ERR_P_FULL);
+              if (!ok) break;
+              if (first) ++o_it[w];
+              ++p_it[w];
+              tc_fence_after();
+              if (!reinterpret_cast<volatile int*>(sm->skip)[w]) {
+                const uint32_t v0 = smem_u32(ring + vs * PA_TILE_BYTES);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  mma_bf16_ts(tmem + 256 + w * 128, tmem + w * 128 + k * 8, smem_desc_sw128(v0 + k * 2048, PA_TILE * 128, 1024),
+                              ID_O, (!first || k > 0) ? 1u : 0u);
+              }
+              mma_commit(&bars.pv_done[w]);
+            }
+            if (j >= it.s[w] && j < it.e[w]) {           // S_w of tile j
+              if (!k_there) ok = mbar_wait(&bars.full[ks], (uint32_t)((kk / PA_SLOTS) & 1), abortp, errp, PA_ERR_K_FULL);
+              k_there = true;
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t q0 = smem_u32(q_s + w * PA_TILE_BYTES), k0 = smem_u32(ring + ks * PA_TILE_BYTES);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                mma_bf16(tmem + w * 128, smem_desc_sw128(q0 + (k >> 2) * (PA_TILE * 128) + (k & 3) * 32, 16, 1024),
+                         smem_desc_sw128(k0 + (k >> 2) * (PA_TILE * 128) + (k & 3) * 32, 16, 1024), ID_S, k > 0 ? 1u : 0u);
+              mma_commit(&bars.s_full[w]);
+            }
+          }
+          if (!ok) break;
+          if (j > it.jb) mma_commit(&bars.empty[vs]);
+          if (j < it.je) mma_commit(&bars.empty[ks]);
+          if (j == it.je - 1) mma_commit(&bars.q_empty); // every S of the item has read Q
+        }
+        kv0 += 2 * (it.je - it.jb);
+      }
+      mma_commit(&bars.final_bar);
+      mbar_wait_done(&bars.final_bar, 0, errp, PA_ERR_FINAL);   // also after an abort: the products finish on their own
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------ softmax + epilogue
+    const int w = warp >> 2;
+    const int row = tid & 127;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lane_off + w * 128, t_o = tmem + lane_off + 256 + w * 128;
+    const float c = sh.scale_log2;
+    int kv0 = 0, t_it = 0, scans = 0;                    // ring position, this Q tile's key tiles, scanned V tiles
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity, int code) -> bool {
+      bool y = true;
+      if (lane == 0) y = mbar_wait(bar, parity, abortp, errp, code);
+      y = __shfl_sync(0xffffffffu, (int)y, 0) != 0;
+      return y;
+    };
+    int4 x;
+    for (int n = 0; ok; ++n) {
+      if (!take_item(n, x)) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.item_empty[n & 1]);
+      const PaItem it = pa_item(sh, cu_q, cu_k, x.x, x.y);
+      const int hk = x.z;
+      const int tw = it.t0 + w * sh.tpt;                 // the Q tile's first token
+      const int ti = row / sh.G, tok = tw + ti;          // this row's token
+      const bool row_ok = ti < it.n[w];
+      const int last = tok + it.off;                     // its last key (below 0: none) and first
+      const int lo = sh.window > 0 ? max(0, last - sh.window + 1) : 0;
+      const int first_last = tw + it.off;                // the tile's first token's last key
+      const int last_lo = sh.window > 0 ? max(0, tw + it.n[w] - 1 + it.off - sh.window + 1) : 0;
+      float m = -INFINITY, l = 0.f;
+      for (int j = it.s[w]; j < it.e[w]; ++j, ++t_it) {
+        if (!wait(&bars.s_full[w], (uint32_t)(t_it & 1), PA_ERR_S_FULL)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t sr[PA_TILE / 32][32];
+#pragma unroll
+        for (int k = 0; k < PA_TILE / 32; ++k) tmem_ld32(t_s + k * 32, sr[k]);
+        tmem_wait_ld();
+        float s[PA_TILE];
+#pragma unroll
+        for (int k = 0; k < PA_TILE; ++k) s[k] = __uint_as_float(sr[k >> 5][k & 31]);
+        const int base = j * PA_TILE;
+        // masked for some token of the Q tile
+        const bool part = base + PA_TILE - 1 > first_last || base < last_lo;
+        if (part) {
+          const int hi = row_ok ? last + 1 - base : PA_TILE, l0 = row_ok ? lo - base : 0;
+#pragma unroll
+          for (int k = 0; k < PA_TILE; ++k) s[k] = k < hi && k >= l0 ? s[k] : -INFINITY;
+        }
+        auto row_max = [&]() -> float {
+          float mx[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx[k] = s[k];
+#pragma unroll
+          for (int k = 8; k < PA_TILE; ++k) mx[k & 7] = fmaxf(mx[k & 7], s[k]);
+          return fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        };
+        if (m == -INFINITY) m = row_max();               // the row's first visible tile sets the reference
+        // P = 2^(c (s - m)) as bf16, two to a column, over the scores. The product
+        // c m may leave fp32 (scores at the type's lowest value): subtract first then
+        auto write_p = [&]() -> float {
+          const float neg = m == -INFINITY ? 0.f : -m * c, ref = m == -INFINITY ? 0.f : m;
+          float ps[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          auto put = [&](auto arg) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t pk[32];
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                const float a = ex2_approx(arg(s[64 * h + 2 * k])), b = ex2_approx(arg(s[64 * h + 2 * k + 1]));
+                ps[(2 * k) & 7] += a;
+                ps[(2 * k + 1) & 7] += b;
+                pk[k] = pack_bf16x2(a, b);
+              }
+              tmem_st32(t_s + h * 32, pk);
+            }
+          };
+          if (__any_sync(0xffffffffu, fabsf(neg) > 1e30f))
+            put([&](float v) { return (v - ref) * c; });
+          else
+            put([&](float v) { return fmaf(v, c, neg); });
+          return ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+        };
+        float sum = write_p();
+        if (__any_sync(0xffffffffu, !(sum <= PA_SUM_MAX))) {
+          // a stale reference: the warp redoes the tile, such rows against its exact maximum, and rescales O and l
+          const bool over = !(sum <= PA_SUM_MAX);
+          float alpha = 1.f;
+          if (over) {
+            const float mx = fmaxf(row_max(), m);
+            alpha = ex2_approx((m - mx) * c);
+            m = mx;
+            l *= alpha;
+          }
+          const float again = write_p();
+          if (over) sum = again;
+          if (j > it.s[w]) {
+            if (!wait(&bars.pv_done[w], (uint32_t)((t_it - 1) & 1), PA_ERR_PV_DONE)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t r[32];
+              tmem_ld32(t_o + k * 32, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+              tmem_st32(t_o + k * 32, r);
+            }
+          }
+        }
+        l += sum;
+        tmem_wait_st();
+        bool redo = false;
+        if (part) {
+          // is the V tile finite? thread = key
+          const int vv = kv0 + 2 * (j - it.jb) + 1, vs = vv % PA_SLOTS;
+          uint8_t* v_s = ring + vs * PA_TILE_BYTES;
+          if (!wait(&bars.full[vs], (uint32_t)((vv / PA_SLOTS) & 1), PA_ERR_V_FULL)) { ok = false; break; }
+          __syncwarp();
+          uint32_t bad = 0u;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const uint4 u = *reinterpret_cast<const uint4*>(v_s + (k >> 3) * (PA_TILE * 128) + row * 128 + (k & 7) * 16);
+            const uint32_t u4[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)                  // an exponent of all ones
+              bad |= (uint32_t)((u4[i] & 0x7f80u) == 0x7f80u) | (uint32_t)((u4[i] & 0x7f800000u) == 0x7f800000u);
+          }
+          volatile int* flag = &sm->bad_v[w][scans & 1];
+          if (__any_sync(0xffffffffu, bad != 0u) && lane == 0) *flag = 1;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.scan[w]);
+          if (!wait(&bars.scan[w], (uint32_t)(scans & 1), PA_ERR_SCAN)) { ok = false; break; }
+          __syncwarp();
+          redo = *flag != 0;
+          // the other parity's flag was read by everyone before this scan's arrivals
+          if (lane == 0 && (warp & 3) == 0) sm->bad_v[w][(scans + 1) & 1] = 0;
+          ++scans;
+          if (redo) {
+            // O += P V here, entries with P = 0 left out
+            if (j > it.s[w] && !wait(&bars.pv_done[w], (uint32_t)((t_it - 1) & 1), PA_ERR_PV_DONE)) { ok = false; break; }
+            tc_fence_after();
+            for (int k = 0; k < 4; ++k) {                // 32 dims at a time
+              uint32_t r[32];
+              if (j > it.s[w]) {
+                tmem_ld32(t_o + k * 32, r);
+                tmem_wait_ld();
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) r[i] = 0u;
+              }
+              for (int key = 0; key < PA_TILE; ++key) {
+                const uint32_t p2 = tmem_ld1(t_s + (key >> 1));
+                tmem_wait_ld();
+                const float p = (key & 1) ? bf16_hi(p2) : bf16_lo(p2);
+                const uint8_t* vr = v_s + (k >> 1) * (PA_TILE * 128);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const uint4 u = *reinterpret_cast<const uint4*>(vr + sw128(key, (k & 1) * 4 + q));
+                  const uint32_t u4[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const int d = q * 8 + 2 * i;
+                    if (p != 0.f) {
+                      r[d] = __float_as_uint(fmaf(p, bf16_lo(u4[i]), __uint_as_float(r[d])));
+                      r[d + 1] = __float_as_uint(fmaf(p, bf16_hi(u4[i]), __uint_as_float(r[d + 1])));
+                    }
+                  }
+                }
+              }
+              tmem_st32(t_o + k * 32, r);
+            }
+            tmem_wait_st();
+          }
+        }
+        if (lane == 0 && (warp & 3) == 0) sm->skip[w] = redo;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[w]);
+      }
+      if (!ok) break;
+      kv0 += 2 * (it.je - it.jb);
+      // ---- epilogue
+      const bool any = it.e[w] > it.s[w];
+      if (any && !wait(&bars.pv_done[w], (uint32_t)((t_it - 1) & 1), PA_ERR_PV_DONE)) break;
+      tc_fence_after();
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const size_t orow = (size_t)(it.q0 + tok) * sh.H + hk * sh.G + (row - ti * sh.G);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t r[32];
+        if (any) {
+          tmem_ld32(t_o + k * 32, r);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = 0u;
+        }
+        if (row_ok) {
+          uint4* dst = reinterpret_cast<uint4*>(out + orow * kD + k * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float f[8];
+            // a row that sees nothing has probabilities 0: its sums are 0
+#pragma unroll
+            for (int q = 0; q < 8; ++q) f[q] = l == 0.f ? 0.f : __uint_as_float(r[8 * i + q]) * inv;
+            dst[i] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                pack_bf16x2(f[6], f[7]));
+          }
+        }
+      }
+      if (row_ok && lse != nullptr) lse[orow] = l == 0.f ? -INFINITY : fmaf(m, sh.scale, log2f(l) * kLn2);
+      if (any) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.o_free[w]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == PA_MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+namespace {
+
+// Q-tile pairs of all sequences at most: a pair for every 2 tpt tokens and one more for each sequence.
+long long pa_most_pairs(int B, int Tq, int tpt) { return (long long)Tq / (2 * tpt) + (B < Tq ? B : Tq); }
+
+}  // namespace
+
+size_t prompt_attn_workspace_bytes(int B, int Tq, int H, int Hkv) {
+  return 16 + (size_t)pa_most_pairs(B, Tq, PA_TILE / (H / Hkv)) * sizeof(int2);
+}
+
+cslc_status launch_prompt_attn(const uint16_t* q, const uint16_t* k, const uint16_t* v, const int32_t* cu_q,
+                               const int32_t* cu_k, int B, int Tq, int Tk, int H, int Hkv, long long q_stride,
+                               long long k_stride, long long v_stride, int window, float scale, uint16_t* out,
+                               float* lse, void* wsp, cudaStream_t stream) {
+  const char* fn = "cslc_prompt_attn";
+  const size_t smem = 1024 + (size_t)(2 + PA_SLOTS) * PA_TILE_BYTES + sizeof(PaSmall);
+  int dev = 0, n_sm = 148;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err == cudaSuccess) err = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  if (err == cudaSuccess)
+    err = cudaFuncSetAttribute(prompt_attn_sm100_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return set_error(CSLC_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(err));
+  const int G = H / Hkv, tpt = PA_TILE / G;
+  const long long items = pa_most_pairs(B, Tq, tpt) * Hkv;
+  const PaShape sh{B, Tq, Tk, H, Hkv, G, tpt, window, scale, scale * kLog2e, items <= n_sm ? 1 : 0};
+  CUtensorMap tm_q, tm_k, tm_v;
+  // without keys no tile of them is loaded: the maps only have to be valid
+  const bool keys = Tk > 0;
+  if (!make_tmap_bf16_rows128(&tm_q, q, H, Tq, q_stride, G, tpt) ||
+      !make_tmap_bf16_rows128(&tm_k, keys ? k : q, keys ? Hkv : H, keys ? Tk : Tq, keys ? k_stride : q_stride, 1, PA_TILE) ||
+      !make_tmap_bf16_rows128(&tm_v, keys ? v : q, keys ? Hkv : H, keys ? Tk : Tq, keys ? v_stride : q_stride, 1, PA_TILE))
+    return set_error(CSLC_ERR_CUDA, "%s: tensor map encoding failed", fn);
+  PaWs ws;
+  ws.head = static_cast<int*>(wsp);
+  ws.list = reinterpret_cast<int2*>(static_cast<uint8_t*>(wsp) + 16);
+  ws.cap = (int)pa_most_pairs(B, Tq, tpt);
+  if (!sh.direct) {
+    prompt_schedule_kernel<<<1, PA_SCHED_THREADS, (size_t)(B + 1) * sizeof(int), stream>>>(sh, cu_q, cu_k, ws);
+    const cslc_status st = check_launch("prompt_schedule_kernel");
+    if (st != CSLC_OK) return st;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items < n_sm ? items : n_sm));
+  cfg.blockDim = dim3(PA_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = sh.direct ? 0 : 1;                      // a dependent of the schedule only
+  err = cudaLaunchKernelEx(&cfg, prompt_attn_sm100_kernel, sh, cu_q, cu_k, ws, out, lse, tm_q, tm_k, tm_v);
+  if (err != cudaSuccess) return set_error(CSLC_ERR_CUDA, "prompt_attn_sm100_kernel: %s", cudaGetErrorString(err));
+  return CSLC_OK;
+}
+
+int prompt_attn_sm100_read_error() {
+  int v = 0, zero = 0;
+  cudaMemcpyFromSymbol(&v, g_prompt_attn_err, sizeof(int));
+  if (v) cudaMemcpyToSymbol(g_prompt_attn_err, &zero, sizeof(int));
+  return v;
+}
+
+CSLC_DEFINE_WAIT_LIMIT_SETTER(prompt_attn_sm100_set_wait_limits)
+
+}  // namespace cslc

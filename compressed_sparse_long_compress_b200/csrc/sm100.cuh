@@ -317,6 +317,10 @@ bool make_tmap_rows3d(CUtensorMap* map, const void* base, int eb, uint64_t n1, u
                       uint32_t box2);
 // rows of 64 bytes (e4m3 codes), 64-byte swizzle, boxes of box_rows x 64
 bool make_tmap_u8_rows64(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows);
+// [n2][n1][128] bf16 with `stride` elements from one outer index to the next,
+// 128-byte swizzle, boxes of 64 x box1 x box2
+bool make_tmap_bf16_rows128(CUtensorMap* map, const void* base, uint64_t n1, uint64_t n2, uint64_t stride, uint32_t box1,
+                            uint32_t box2);
 // rows of 128 bytes (e4m3 codes), 128-byte swizzle, boxes of box_rows x 128
 bool make_tmap_u8_rows128(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows);
 

@@ -451,7 +451,7 @@ cslc_status cslc_page_write_e4m3(const cslc_bf16* k, const cslc_bf16* v, const i
  *   out [Tq, H, 128] bf16; lse [Tq, H] fp32 (natural log-sum-exp), or NULL
  *   ws  workspace of cslc_prompt_attn_workspace_bytes() bytes; it belongs to
  *       one call at a time (also in captured graphs)
- * 0 <= B <= 8192, window >= 0. */
+ * 0 <= B <= 8192, window >= 0, scale positive and finite. */
 size_t cslc_prompt_attn_workspace_bytes(int B, int Tq, int H, int Hkv);
 cslc_status cslc_prompt_attn(const cslc_bf16* q, const cslc_bf16* k, const cslc_bf16* v, const int32_t* cu_q,
                              const int32_t* cu_k, int B, int Tq, int Tk, int H, int Hkv, int D, int64_t q_stride,
@@ -471,7 +471,7 @@ cslc_status cslc_prompt_attn(const cslc_bf16* q, const cslc_bf16* k, const cslc_
  *   out [B, H, 128] bf16; lse [B, H] fp32, or NULL
  *   ws  workspace of cslc_page_decode_workspace_bytes() bytes; it belongs to
  *       one call at a time (also in captured graphs)
- * 0 <= B <= 8192, window >= 0. */
+ * 0 <= B <= 8192, window >= 0, scale positive and finite. */
 size_t cslc_page_decode_workspace_bytes(int B, int H, int Hkv);
 cslc_status cslc_page_decode_attn(const cslc_bf16* q, const uint8_t* k_cache, const uint8_t* v_cache,
                                   const float* k_scale, const float* v_scale, const int32_t* block_table,

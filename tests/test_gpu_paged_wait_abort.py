@@ -49,3 +49,14 @@ def test_decode_wait_abort_then_recovers(C, H):
     kc, vc, ks, vs = (x.cpu().numpy() for x in cache)
     ref = PO.page_decode_attention(TP.f64(q), kc, vc, ks.astype(float), vs.astype(float), table.cpu().numpy(), lens, TP.SCALE)
     TP.check_attention(out, lse, ref, max(lens), "decode after an abort")
+
+
+def test_prompt_wait_abort_then_recovers(C):
+    q, k, v = TP.randn((3000, 8, 128), 1), TP.randn((3000, 2, 128), 2), TP.randn((3000, 2, 128), 3)
+    cu = [0, 1700, 3000]
+    run = lambda: C.prompt_attn(q, k, v, TP.i32(cu), TP.i32(cu), TP.SCALE, lse=True)  # noqa: E731
+    _aborts(C, run, "cslc_prompt_attn")
+    out, lse = run()
+    C.sync_status()
+    ref = PO.prompt_attention(TP.f64(q), TP.f64(k), TP.f64(v), cu, cu, TP.SCALE, rows={0, 5, 1699, 1700, 1701, 2999})
+    TP.check_attention(out, lse, ref, 1700, "prompt after an abort")
