@@ -56,12 +56,12 @@ constexpr int PA_BUCKETS = 512;
 constexpr int PA_SCHED_THREADS = 1024;
 
 enum { PA_ERR_ITEM = 1, PA_ERR_Q_EMPTY, PA_ERR_EMPTY, PA_ERR_Q_FULL, PA_ERR_K_FULL, PA_ERR_V_FULL, PA_ERR_P_FULL,
-       PA_ERR_O_FREE, PA_ERR_S_FULL, PA_ERR_PV_DONE, PA_ERR_SCAN, PA_ERR_FINAL };
+       PA_ERR_O_FREE, PA_ERR_S_FULL, PA_ERR_PV_HALF, PA_ERR_O_FULL, PA_ERR_SCAN, PA_ERR_FINAL };
 
 struct __align__(8) PaBars {
   uint64_t full[PA_SLOTS], empty[PA_SLOTS];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2], scan[2];
+  uint64_t s_full[2], p_full[2][2], pv_half[2], o_full[2], o_free[2], scan[2];
   uint64_t item_full[2], item_empty[2];
   uint64_t final_bar;
 };
@@ -131,6 +131,25 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+// The wait for 64 columns' values; they are tied to it, so that no use of them moves in front of it.
+__device__ __forceinline__ void tmem_wait_ld64(uint32_t (&r)[2][32]) {
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[0][i]), "+r"(r[1][i]));
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
 }
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
   uint32_t r;
@@ -246,8 +265,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
     for (int s = 0; s < PA_SLOTS; ++s) { mbar_init(&bars.full[s], 1); mbar_init(&bars.empty[s], 1); }
     mbar_init(&bars.q_full, 1); mbar_init(&bars.q_empty, 1);
     for (int w = 0; w < 2; ++w) {
-      mbar_init(&bars.s_full[w], 1); mbar_init(&bars.p_full[w], 4); mbar_init(&bars.pv_done[w], 1);
-      mbar_init(&bars.o_free[w], 4); mbar_init(&bars.scan[w], 4);
+      mbar_init(&bars.s_full[w], 1); mbar_init(&bars.p_full[w][0], 4); mbar_init(&bars.p_full[w][1], 4);
+      mbar_init(&bars.pv_half[w], 1); mbar_init(&bars.o_full[w], 1); mbar_init(&bars.o_free[w], 4); mbar_init(&bars.scan[w], 4);
       mbar_init(&bars.item_full[w], 1); mbar_init(&bars.item_empty[w], 9);
       sm->skip[w] = 0;
       sm->bad_v[w][0] = sm->bad_v[w][1] = 0;
@@ -357,6 +376,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
     if (lane == 0) {
       constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false);
       constexpr uint32_t ID_O = idesc_bf16(128, 128, false, true);
+      // descriptors of Q tile 0, and of ring slot 0 as K and as V; an offset of x bytes adds x / 16
+      const uint64_t dq = smem_desc_sw128(smem_u32(q_s), 16, 1024);
+      const uint64_t dk = smem_desc_sw128(smem_u32(ring), 16, 1024);
+      const uint64_t dv = smem_desc_sw128(smem_u32(ring), PA_TILE * 128, 1024);
       int kv0 = 0;                                       // ring position of the item's first K
       int p_it[2] = {0, 0}, o_it[2] = {0, 0};            // P tiles taken, items with a tile
       bool ok = true;
@@ -374,37 +397,45 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
           const int kk = kv0 + 2 * (j - it.jb), vv = kk - 1;
           const int ks = kk % PA_SLOTS, vs = j > it.jb ? vv % PA_SLOTS : 0;
           bool k_there = false, v_there = false;
-          for (int w = 0; w < 2 && ok; ++w) {
-            if (j > it.s[w] && j <= it.e[w]) {           // P_w V of tile j - 1
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (!ok) break;
+            if (j > it.s[w] && j <= it.e[w]) {           // P_w V of tile j - 1, 64 keys at a time
               if (!v_there) ok = mbar_wait(&bars.full[vs], (uint32_t)((vv / PA_SLOTS) & 1), abortp, errp, PA_ERR_V_FULL);
               v_there = true;
               const bool first = j - 1 == it.s[w];
               if (ok && first && o_it[w] > 0)
                 ok = mbar_wait(&bars.o_free[w], (uint32_t)((o_it[w] - 1) & 1), abortp, errp, PA_ERR_O_FREE);
-              if (ok) ok = mbar_wait(&bars.p_full[w], (uint32_t)(p_it[w] & 1), abortp, errp, PA_ERR_P_FULL);
-              if (!ok) break;
               if (first) ++o_it[w];
-              ++p_it[w];
-              tc_fence_after();
-              if (!reinterpret_cast<volatile int*>(sm->skip)[w]) {
-                const uint32_t v0 = smem_u32(ring + vs * PA_TILE_BYTES);
+              const uint64_t d = dv + (uint64_t)(vs * (PA_TILE_BYTES / 16));
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  mma_bf16_ts(tmem + 256 + w * 128, tmem + w * 128 + k * 8, smem_desc_sw128(v0 + k * 2048, PA_TILE * 128, 1024),
-                              ID_O, (!first || k > 0) ? 1u : 0u);
+              for (int h = 0; h < 2; ++h) {
+                if (ok) ok = mbar_wait(&bars.p_full[w][h], (uint32_t)(p_it[w] & 1), abortp, errp, PA_ERR_P_FULL);
+                if (!ok) break;
+                tc_fence_after();
+                if (!reinterpret_cast<volatile int*>(sm->skip)[w]) {
+#pragma unroll
+                  for (int k = 4 * h; k < 4 * h + 4; ++k)
+                    mma_bf16_ts(tmem + 256 + w * 128, tmem + w * 128 + k * 8, d + k * (2048 / 16), ID_O,
+                                (!first || k > 0) ? 1u : 0u);
+                }
+                if (h == 0) mma_commit(&bars.pv_half[w]);
               }
-              mma_commit(&bars.pv_done[w]);
+              if (!ok) break;
+              ++p_it[w];
+              if (j == it.e[w]) mma_commit(&bars.o_full[w]);
             }
             if (j >= it.s[w] && j < it.e[w]) {           // S_w of tile j
               if (!k_there) ok = mbar_wait(&bars.full[ks], (uint32_t)((kk / PA_SLOTS) & 1), abortp, errp, PA_ERR_K_FULL);
               k_there = true;
               if (!ok) break;
               tc_fence_after();
-              const uint32_t q0 = smem_u32(q_s + w * PA_TILE_BYTES), k0 = smem_u32(ring + ks * PA_TILE_BYTES);
+              const uint64_t a = dq + (uint64_t)(w * (PA_TILE_BYTES / 16)), d = dk + (uint64_t)(ks * (PA_TILE_BYTES / 16));
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                mma_bf16(tmem + w * 128, smem_desc_sw128(q0 + (k >> 2) * (PA_TILE * 128) + (k & 3) * 32, 16, 1024),
-                         smem_desc_sw128(k0 + (k >> 2) * (PA_TILE * 128) + (k & 3) * 32, 16, 1024), ID_S, k > 0 ? 1u : 0u);
+              for (int k = 0; k < 8; ++k) {
+                const uint64_t off = ((k >> 2) * (PA_TILE * 128) + (k & 3) * 32) / 16;
+                mma_bf16(tmem + w * 128, a + off, d + off, ID_S, k > 0 ? 1u : 0u);
+              }
               mma_commit(&bars.s_full[w]);
             }
           }
@@ -426,13 +457,78 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_off + w * 128, t_o = tmem + lane_off + 256 + w * 128;
     const float c = sh.scale_log2;
-    int kv0 = 0, t_it = 0, scans = 0;                    // ring position, this Q tile's key tiles, scanned V tiles
+    int kv0 = 0, t_it = 0, scans = 0, o_it = 0;          // ring position, this Q tile's key tiles, scans, items
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity, int code) -> bool {
       bool y = true;
       if (lane == 0) y = mbar_wait(bar, parity, abortp, errp, code);
       y = __shfl_sync(0xffffffffu, (int)y, 0) != 0;
       return y;
+    };
+    // is the V tile at ring position vv finite (slow = false)? thread = key; all four warps agree
+    auto scan_v = [&](int vv, bool& slow) -> bool {
+      const int vs = vv % PA_SLOTS;
+      const uint8_t* v_s = ring + vs * PA_TILE_BYTES;
+      if (!wait(&bars.full[vs], (uint32_t)((vv / PA_SLOTS) & 1), PA_ERR_V_FULL)) return false;
+      __syncwarp();
+      uint32_t bad = 0u;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const uint4 u = *reinterpret_cast<const uint4*>(v_s + (k >> 3) * (PA_TILE * 128) + row * 128 + (((k & 7) ^ (row & 7)) << 4));
+        const uint32_t u4[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)                      // an exponent of all ones
+          bad |= (uint32_t)((u4[i] & 0x7f80u) == 0x7f80u) | (uint32_t)((u4[i] & 0x7f800000u) == 0x7f800000u);
+      }
+      volatile int* flag = &sm->bad_v[w][scans & 1];
+      if (__any_sync(0xffffffffu, bad != 0u) && lane == 0) *flag = 1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.scan[w]);
+      if (!wait(&bars.scan[w], (uint32_t)(scans & 1), PA_ERR_SCAN)) return false;
+      __syncwarp();
+      slow = *flag != 0;
+      // the other parity's flag was read by everyone before this scan's arrivals, and the next
+      // scan waits for a tile that needs this warp
+      if (lane == 0 && (warp & 3) == 0) sm->bad_v[w][(scans + 1) & 1] = 0;
+      ++scans;
+      return true;
+    };
+    // O += P V on the CUDA cores, entries with P = 0 left out; the tensor cores' products are done
+    auto slow_pv = [&](int vv, bool first) {
+      const uint8_t* v_s = ring + (vv % PA_SLOTS) * PA_TILE_BYTES;
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {                      // 32 dims at a time
+        uint32_t r[32];
+        if (!first) {
+          tmem_ld32(t_o + k * 32, r);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = 0u;
+        }
+#pragma unroll 1
+        for (int key = 0; key < PA_TILE; ++key) {
+          const uint32_t p2 = tmem_ld1(t_s + (key >> 1));
+          tmem_wait_ld();
+          const float p = (key & 1) ? bf16_hi(p2) : bf16_lo(p2);
+          const uint8_t* vr = v_s + (k >> 1) * (PA_TILE * 128);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint4 u = *reinterpret_cast<const uint4*>(vr + sw128(key, (k & 1) * 4 + q));
+            const uint32_t u4[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int d = q * 8 + 2 * i;
+              if (p != 0.f) {
+                r[d] = __float_as_uint(fmaf(p, bf16_lo(u4[i]), __uint_as_float(r[d])));
+                r[d + 1] = __float_as_uint(fmaf(p, bf16_hi(u4[i]), __uint_as_float(r[d + 1])));
+              }
+            }
+          }
+        }
+        tmem_st32(t_o + k * 32, r);
+      }
+      tmem_wait_st();
     };
     int4 x;
     for (int n = 0; ok; ++n) {
@@ -450,159 +546,116 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       const int last_lo = sh.window > 0 ? max(0, tw + it.n[w] - 1 + it.off - sh.window + 1) : 0;
       float m = -INFINITY, l = 0.f;
       for (int j = it.s[w]; j < it.e[w]; ++j, ++t_it) {
-        if (!wait(&bars.s_full[w], (uint32_t)(t_it & 1), PA_ERR_S_FULL)) { ok = false; break; }
-        tc_fence_after();
-        uint32_t sr[PA_TILE / 32][32];
-#pragma unroll
-        for (int k = 0; k < PA_TILE / 32; ++k) tmem_ld32(t_s + k * 32, sr[k]);
-        tmem_wait_ld();
-        float s[PA_TILE];
-#pragma unroll
-        for (int k = 0; k < PA_TILE; ++k) s[k] = __uint_as_float(sr[k >> 5][k & 31]);
         const int base = j * PA_TILE;
         // masked for some token of the Q tile
         const bool part = base + PA_TILE - 1 > first_last || base < last_lo;
-        if (part) {
-          const int hi = row_ok ? last + 1 - base : PA_TILE, l0 = row_ok ? lo - base : 0;
+        const int hi = part && row_ok ? last + 1 - base : PA_TILE, l0 = part && row_ok ? lo - base : 0;
+        bool slow = false;
+        if (part && !scan_v(kv0 + 2 * (j - it.jb) + 1, slow)) { ok = false; break; }
+        // s_full(j) also says that every product before S_w(j) is done, PV_w(j - 1) among them
+        if (!wait(&bars.s_full[w], (uint32_t)(t_it & 1), PA_ERR_S_FULL)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t s[2][32];
+        auto at = [&](int k) { return __uint_as_float(s[k >> 5][k & 31]); };
+        auto load = [&](int h) {                         // the scores of 64 keys, masked
+          tmem_ld32(t_s + 64 * h, s[0]);
+          tmem_ld32(t_s + 64 * h + 32, s[1]);
+          tmem_wait_ld64(s);
+          if (part) {
 #pragma unroll
-          for (int k = 0; k < PA_TILE; ++k) s[k] = k < hi && k >= l0 ? s[k] : -INFINITY;
-        }
+            for (int k = 0; k < 64; ++k)
+              s[k >> 5][k & 31] = 64 * h + k < hi && 64 * h + k >= l0 ? s[k >> 5][k & 31] : 0xff800000u;
+          }
+        };
         auto row_max = [&]() -> float {
-          float mx[8];
+          float mx[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mx[k] = s[k];
+          for (int k = 0; k < 4; ++k) mx[k] = at(k);
 #pragma unroll
-          for (int k = 8; k < PA_TILE; ++k) mx[k & 7] = fmaxf(mx[k & 7], s[k]);
-          return fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+          for (int k = 4; k < 64; ++k) mx[k & 3] = fmaxf(mx[k & 3], at(k));
+          return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         };
-        if (m == -INFINITY) m = row_max();               // the row's first visible tile sets the reference
-        // P = 2^(c (s - m)) as bf16, two to a column, over the scores. The product
-        // c m may leave fp32 (scores at the type's lowest value): subtract first then
-        auto write_p = [&]() -> float {
-          const float neg = m == -INFINITY ? 0.f : -m * c, ref = m == -INFINITY ? 0.f : m;
-          float ps[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          auto put = [&](auto arg) {
+        auto rescale = [&](float mx) {                   // to the reference mx >= m
+          const float alpha = mx > m ? ex2_approx((m - mx) * c) : 1.f;
+          m = fmaxf(m, mx);
+          l *= alpha;
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            uint32_t r[32];
+            tmem_ld32(t_o + k * 32, r);
+            tmem_wait_ld();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t pk[32];
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                const float a = ex2_approx(arg(s[64 * h + 2 * k])), b = ex2_approx(arg(s[64 * h + 2 * k + 1]));
-                ps[(2 * k) & 7] += a;
-                ps[(2 * k + 1) & 7] += b;
-                pk[k] = pack_bf16x2(a, b);
-              }
-              tmem_st32(t_s + h * 32, pk);
-            }
-          };
-          if (__any_sync(0xffffffffu, fabsf(neg) > 1e30f))
-            put([&](float v) { return (v - ref) * c; });
-          else
-            put([&](float v) { return fmaf(v, c, neg); });
-          return ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
-        };
-        float sum = write_p();
-        if (__any_sync(0xffffffffu, !(sum <= PA_SUM_MAX))) {
-          // a stale reference: the warp redoes the tile, such rows against its exact maximum, and rescales O and l
-          const bool over = !(sum <= PA_SUM_MAX);
-          float alpha = 1.f;
-          if (over) {
-            const float mx = fmaxf(row_max(), m);
-            alpha = ex2_approx((m - mx) * c);
-            m = mx;
-            l *= alpha;
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+            tmem_st32(t_o + k * 32, r);
           }
-          const float again = write_p();
-          if (over) sum = again;
-          if (j > it.s[w]) {
-            if (!wait(&bars.pv_done[w], (uint32_t)((t_it - 1) & 1), PA_ERR_PV_DONE)) { ok = false; break; }
-            tc_fence_after();
+        };
+        if (slow) {                                      // the whole tile's maximum first: no redo later
+          load(0);
+          float mx = row_max();
+          load(1);
+          mx = fmaxf(mx, row_max());
+          if (m == -INFINITY) m = mx;
+          if (j > it.s[w]) rescale(mx);
+        }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t r[32];
-              tmem_ld32(t_o + k * 32, r);
-              tmem_wait_ld();
+        for (int h = 0; h < 2; ++h) {
+          load(h);
+          if (m == -INFINITY) m = row_max();             // the row's first visible keys set the reference
+          // P = 2^(c (s - m)) as bf16, two to a column, over the scores that were read
+          const float neg = m == -INFINITY ? 0.f : -m * c;
+          float2 ps[4];
+          uint32_t pk[32];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-              tmem_st32(t_o + k * 32, r);
+          for (int k = 0; k < 4; ++k) ps[k] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            float2 a = fma2(make_float2(at(2 * k), at(2 * k + 1)), make_float2(c, c),
+                            make_float2(neg, neg));
+            a = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+            ps[k & 3] = add2(ps[k & 3], a);
+            pk[k] = pack_bf16x2(a.x, a.y);
+          }
+          ps[0] = add2(add2(ps[0], ps[1]), add2(ps[2], ps[3]));
+          float sum = ps[0].x + ps[0].y;
+          // a stale reference (the probabilities leave the range), or c m does: the warp redoes these keys
+          const bool over = !(sum <= PA_SUM_MAX), far = fabsf(neg) > 1e30f;
+          if (__any_sync(0xffffffffu, over || far)) {
+            if (!slow && (h == 1 || j > it.s[w])) {
+              if (h == 1 && !wait(&bars.pv_half[w], (uint32_t)(t_it & 1), PA_ERR_PV_HALF)) { ok = false; break; }
+              tc_fence_after();
+              rescale(over ? row_max() : m);
+            } else if (over) {
+              m = fmaxf(m, row_max());
             }
+            const float ref = m == -INFINITY ? 0.f : m;
+            sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float a = ex2_approx((at(2 * k) - ref) * c);
+              const float b = ex2_approx((at(2 * k + 1) - ref) * c);
+              sum += a + b;
+              pk[k] = pack_bf16x2(a, b);
+            }
+          }
+          l += sum;
+          tmem_st32(t_s + 32 * h, pk);
+          tmem_wait_st();
+          if (slow && h == 1) slow_pv(kv0 + 2 * (j - it.jb) + 1, j == it.s[w]);
+          if (lane == 0 && (warp & 3) == 0) sm->skip[w] = slow;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0 && (!slow || h == 1)) {
+            if (slow) mbar_arrive(&bars.p_full[w][0]);
+            mbar_arrive(&bars.p_full[w][h]);
           }
         }
-        l += sum;
-        tmem_wait_st();
-        bool redo = false;
-        if (part) {
-          // is the V tile finite? thread = key
-          const int vv = kv0 + 2 * (j - it.jb) + 1, vs = vv % PA_SLOTS;
-          uint8_t* v_s = ring + vs * PA_TILE_BYTES;
-          if (!wait(&bars.full[vs], (uint32_t)((vv / PA_SLOTS) & 1), PA_ERR_V_FULL)) { ok = false; break; }
-          __syncwarp();
-          uint32_t bad = 0u;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const uint4 u = *reinterpret_cast<const uint4*>(v_s + (k >> 3) * (PA_TILE * 128) + row * 128 + (k & 7) * 16);
-            const uint32_t u4[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)                  // an exponent of all ones
-              bad |= (uint32_t)((u4[i] & 0x7f80u) == 0x7f80u) | (uint32_t)((u4[i] & 0x7f800000u) == 0x7f800000u);
-          }
-          volatile int* flag = &sm->bad_v[w][scans & 1];
-          if (__any_sync(0xffffffffu, bad != 0u) && lane == 0) *flag = 1;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.scan[w]);
-          if (!wait(&bars.scan[w], (uint32_t)(scans & 1), PA_ERR_SCAN)) { ok = false; break; }
-          __syncwarp();
-          redo = *flag != 0;
-          // the other parity's flag was read by everyone before this scan's arrivals
-          if (lane == 0 && (warp & 3) == 0) sm->bad_v[w][(scans + 1) & 1] = 0;
-          ++scans;
-          if (redo) {
-            // O += P V here, entries with P = 0 left out
-            if (j > it.s[w] && !wait(&bars.pv_done[w], (uint32_t)((t_it - 1) & 1), PA_ERR_PV_DONE)) { ok = false; break; }
-            tc_fence_after();
-            for (int k = 0; k < 4; ++k) {                // 32 dims at a time
-              uint32_t r[32];
-              if (j > it.s[w]) {
-                tmem_ld32(t_o + k * 32, r);
-                tmem_wait_ld();
-              } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) r[i] = 0u;
-              }
-              for (int key = 0; key < PA_TILE; ++key) {
-                const uint32_t p2 = tmem_ld1(t_s + (key >> 1));
-                tmem_wait_ld();
-                const float p = (key & 1) ? bf16_hi(p2) : bf16_lo(p2);
-                const uint8_t* vr = v_s + (k >> 1) * (PA_TILE * 128);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const uint4 u = *reinterpret_cast<const uint4*>(vr + sw128(key, (k & 1) * 4 + q));
-                  const uint32_t u4[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const int d = q * 8 + 2 * i;
-                    if (p != 0.f) {
-                      r[d] = __float_as_uint(fmaf(p, bf16_lo(u4[i]), __uint_as_float(r[d])));
-                      r[d + 1] = __float_as_uint(fmaf(p, bf16_hi(u4[i]), __uint_as_float(r[d + 1])));
-                    }
-                  }
-                }
-              }
-              tmem_st32(t_o + k * 32, r);
-            }
-            tmem_wait_st();
-          }
-        }
-        if (lane == 0 && (warp & 3) == 0) sm->skip[w] = redo;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full[w]);
+        if (!ok) break;
       }
       if (!ok) break;
       kv0 += 2 * (it.je - it.jb);
       // ---- epilogue
       const bool any = it.e[w] > it.s[w];
-      if (any && !wait(&bars.pv_done[w], (uint32_t)((t_it - 1) & 1), PA_ERR_PV_DONE)) break;
+      if (any && !wait(&bars.o_full[w], (uint32_t)(o_it++ & 1), PA_ERR_O_FULL)) break;
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const size_t orow = (size_t)(it.q0 + tok) * sh.H + hk * sh.G + (row - ti * sh.G);
