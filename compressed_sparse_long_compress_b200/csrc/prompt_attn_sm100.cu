@@ -138,6 +138,12 @@ __device__ __forceinline__ void tmem_wait_ld64(uint32_t (&r)[2][32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[0][i]), "+r"(r[1][i]));
 }
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   uint64_t d;
@@ -373,80 +379,102 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
     __syncwarp();
   } else if (warp == PA_MMA_WARP) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    // The whole warp walks the loop and one elected lane issues: descriptors stay
+    // in uniform registers (a lone thread took 77-88 cycles for a product of 64).
+    {
       constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false);
       constexpr uint32_t ID_O = idesc_bf16(128, 128, false, true);
-      // descriptors of Q tile 0, and of ring slot 0 as K and as V; an offset of x bytes adds x / 16
-      const uint64_t dq = smem_desc_sw128(smem_u32(q_s), 16, 1024);
-      const uint64_t dk = smem_desc_sw128(smem_u32(ring), 16, 1024);
-      const uint64_t dv = smem_desc_sw128(smem_u32(ring), PA_TILE * 128, 1024);
-      int kv0 = 0;                                       // ring position of the item's first K
+      // low words of the descriptors of Q tile 0 and ring slot 0; an offset of x bytes adds x / 16
+      const uint64_t d_kmaj = smem_desc_sw128(0, 16, 1024), d_mnmaj = smem_desc_sw128(0, PA_TILE * 128, 1024);
+      const uint32_t q0 = smem_u32(q_s) >> 4, r0 = smem_u32(ring) >> 4;
+      auto uni = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
+      int ks = 0, kph = 0;                               // ring slot and phase of the next K
+      auto step = [](int& slot, int& ph) { if (++slot == PA_SLOTS) { slot = 0; ph ^= 1; } };
       int p_it[2] = {0, 0}, o_it[2] = {0, 0};            // P tiles taken, items with a tile
       bool ok = true;
-      int4 x;
       for (int n = 0; ok; ++n) {
         if (!mbar_wait(&bars.item_full[n & 1], (uint32_t)((n >> 1) & 1), abortp, errp, PA_ERR_ITEM)) break;
-        x = sm->item[n & 1];
-        mbar_arrive(&bars.item_empty[n & 1]);
+        const int4 x = sm->item[n & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.item_empty[n & 1]);
         if (x.x < 0) break;
-        const PaItem it = pa_item(sh, cu_q, cu_k, x.x, x.y);
+        PaItem it = pa_item(sh, cu_q, cu_k, x.x, x.y);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) { it.s[w] = uni(it.s[w]); it.e[w] = uni(it.e[w]); }
+        const int jb = uni(it.jb), je = uni(it.je);
         if (!mbar_wait(&bars.q_full, (uint32_t)(n & 1), abortp, errp, PA_ERR_Q_FULL)) break;
-        if (it.jb == it.je) { mma_commit(&bars.q_empty); continue; }
-        // ring position of K_j: kv0 + 2 (j - jb), of V_j the one behind it
-        for (int j = it.jb; j <= it.je && ok; ++j) {
-          const int kk = kv0 + 2 * (j - it.jb), vv = kk - 1;
-          const int ks = kk % PA_SLOTS, vs = j > it.jb ? vv % PA_SLOTS : 0;
+        if (jb == je) {
+          if (elect_one()) mma_commit(&bars.q_empty);
+          continue;
+        }
+        int vs = 0, vph = 0;                             // V_(j - 1)
+        for (int j = jb; j <= je; ++j) {
           bool k_there = false, v_there = false;
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            if (!ok) break;
             if (j > it.s[w] && j <= it.e[w]) {           // P_w V of tile j - 1, 64 keys at a time
-              if (!v_there) ok = mbar_wait(&bars.full[vs], (uint32_t)((vv / PA_SLOTS) & 1), abortp, errp, PA_ERR_V_FULL);
+              if (!v_there) ok = ok && mbar_wait(&bars.full[vs], (uint32_t)vph, abortp, errp, PA_ERR_V_FULL);
               v_there = true;
               const bool first = j - 1 == it.s[w];
-              if (ok && first && o_it[w] > 0)
-                ok = mbar_wait(&bars.o_free[w], (uint32_t)((o_it[w] - 1) & 1), abortp, errp, PA_ERR_O_FREE);
+              if (first && o_it[w] > 0)
+                ok = ok && mbar_wait(&bars.o_free[w], (uint32_t)((o_it[w] - 1) & 1), abortp, errp, PA_ERR_O_FREE);
               if (first) ++o_it[w];
-              const uint64_t d = dv + (uint64_t)(vs * (PA_TILE_BYTES / 16));
+              const uint32_t lo = uni(r0 + vs * (PA_TILE_BYTES / 16));
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                if (ok) ok = mbar_wait(&bars.p_full[w][h], (uint32_t)(p_it[w] & 1), abortp, errp, PA_ERR_P_FULL);
+                ok = ok && mbar_wait(&bars.p_full[w][h], (uint32_t)(p_it[w] & 1), abortp, errp, PA_ERR_P_FULL);
                 if (!ok) break;
                 tc_fence_after();
-                if (!reinterpret_cast<volatile int*>(sm->skip)[w]) {
+                const bool mine = !reinterpret_cast<volatile int*>(sm->skip)[w];
+                if (elect_one()) {
+                  if (mine) {
 #pragma unroll
-                  for (int k = 4 * h; k < 4 * h + 4; ++k)
-                    mma_bf16_ts(tmem + 256 + w * 128, tmem + w * 128 + k * 8, d + k * (2048 / 16), ID_O,
-                                (!first || k > 0) ? 1u : 0u);
+                    for (int k = 4 * h; k < 4 * h + 4; ++k)
+                      mma_bf16_ts(tmem + 256 + w * 128, tmem + w * 128 + k * 8, d_mnmaj | (lo + k * (2048 / 16)), ID_O,
+                                  (!first || k > 0) ? 1u : 0u);
+                  }
+                  if (h == 0) mma_commit(&bars.pv_half[w]);
+                  else if (j == it.e[w]) mma_commit(&bars.o_full[w]);
                 }
-                if (h == 0) mma_commit(&bars.pv_half[w]);
+                __syncwarp();
               }
               if (!ok) break;
               ++p_it[w];
-              if (j == it.e[w]) mma_commit(&bars.o_full[w]);
             }
             if (j >= it.s[w] && j < it.e[w]) {           // S_w of tile j
-              if (!k_there) ok = mbar_wait(&bars.full[ks], (uint32_t)((kk / PA_SLOTS) & 1), abortp, errp, PA_ERR_K_FULL);
+              if (!k_there) ok = mbar_wait(&bars.full[ks], (uint32_t)kph, abortp, errp, PA_ERR_K_FULL);
               k_there = true;
               if (!ok) break;
               tc_fence_after();
-              const uint64_t a = dq + (uint64_t)(w * (PA_TILE_BYTES / 16)), d = dk + (uint64_t)(ks * (PA_TILE_BYTES / 16));
+              const uint32_t la = q0 + w * (PA_TILE_BYTES / 16), lb = uni(r0 + ks * (PA_TILE_BYTES / 16));
+              if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const uint64_t off = ((k >> 2) * (PA_TILE * 128) + (k & 3) * 32) / 16;
-                mma_bf16(tmem + w * 128, a + off, d + off, ID_S, k > 0 ? 1u : 0u);
+                for (int k = 0; k < 8; ++k) {
+                  const uint32_t off = ((k >> 2) * (PA_TILE * 128) + (k & 3) * 32) / 16;
+                  mma_bf16(tmem + w * 128, d_kmaj | (la + off), d_kmaj | (lb + off), ID_S, k > 0 ? 1u : 0u);
+                }
+                mma_commit(&bars.s_full[w]);
               }
-              mma_commit(&bars.s_full[w]);
+              __syncwarp();
             }
           }
           if (!ok) break;
-          if (j > it.jb) mma_commit(&bars.empty[vs]);
-          if (j < it.je) mma_commit(&bars.empty[ks]);
-          if (j == it.je - 1) mma_commit(&bars.q_empty); // every S of the item has read Q
+          if (elect_one()) {
+            if (j > jb) mma_commit(&bars.empty[vs]);
+            if (j < je) mma_commit(&bars.empty[ks]);
+            if (j == je - 1) mma_commit(&bars.q_empty);  // every S of the item has read Q
+          }
+          __syncwarp();
+          if (j < je) {                                  // the V behind this K, then the next K
+            vs = ks; vph = kph;
+            step(vs, vph);
+            ks = vs; kph = vph;
+            step(ks, kph);
+          }
         }
-        kv0 += 2 * (it.je - it.jb);
       }
-      mma_commit(&bars.final_bar);
+      if (elect_one()) mma_commit(&bars.final_bar);
+      __syncwarp();
       mbar_wait_done(&bars.final_bar, 0, errp, PA_ERR_FINAL);   // also after an abort: the products finish on their own
     }
     __syncwarp();
