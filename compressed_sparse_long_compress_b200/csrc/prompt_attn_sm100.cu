@@ -407,25 +407,25 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
           if (elect_one()) mma_commit(&bars.q_empty);
           continue;
         }
-        int vs = 0, vph = 0;                             // V_(j - 1)
-        for (int j = jb; j <= je; ++j) {
-          bool k_there = false, v_there = false;
+        // V_(j - 1), K_j and V_j, K_(j + 1) are waited for while the products issued last still run
+        int vs = 0;                                      // ring slot of V_(j - 1)
+        ok = mbar_wait(&bars.full[ks], (uint32_t)kph, abortp, errp, PA_ERR_K_FULL);
+        for (int j = jb; j <= je && ok; ++j) {
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (j > it.s[w] && j <= it.e[w]) {           // P_w V of tile j - 1, 64 keys at a time
-              if (!v_there) ok = ok && mbar_wait(&bars.full[vs], (uint32_t)vph, abortp, errp, PA_ERR_V_FULL);
-              v_there = true;
               const bool first = j - 1 == it.s[w];
               if (first && o_it[w] > 0)
                 ok = ok && mbar_wait(&bars.o_free[w], (uint32_t)((o_it[w] - 1) & 1), abortp, errp, PA_ERR_O_FREE);
               if (first) ++o_it[w];
               const uint32_t lo = uni(r0 + vs * (PA_TILE_BYTES / 16));
+              bool mine = true;
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 ok = ok && mbar_wait(&bars.p_full[w][h], (uint32_t)(p_it[w] & 1), abortp, errp, PA_ERR_P_FULL);
                 if (!ok) break;
                 tc_fence_after();
-                const bool mine = !reinterpret_cast<volatile int*>(sm->skip)[w];
+                if (h == 0) mine = !reinterpret_cast<volatile int*>(sm->skip)[w];
                 if (elect_one()) {
                   if (mine) {
 #pragma unroll
@@ -442,9 +442,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
               ++p_it[w];
             }
             if (j >= it.s[w] && j < it.e[w]) {           // S_w of tile j
-              if (!k_there) ok = mbar_wait(&bars.full[ks], (uint32_t)kph, abortp, errp, PA_ERR_K_FULL);
-              k_there = true;
-              if (!ok) break;
               tc_fence_after();
               const uint32_t la = q0 + w * (PA_TILE_BYTES / 16), lb = uni(r0 + ks * (PA_TILE_BYTES / 16));
               if (elect_one()) {
@@ -466,10 +463,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
           }
           __syncwarp();
           if (j < je) {                                  // the V behind this K, then the next K
-            vs = ks; vph = kph;
-            step(vs, vph);
-            ks = vs; kph = vph;
             step(ks, kph);
+            vs = ks;
+            ok = mbar_wait(&bars.full[ks], (uint32_t)kph, abortp, errp, PA_ERR_V_FULL);
+            step(ks, kph);
+            if (j + 1 < je) ok = ok && mbar_wait(&bars.full[ks], (uint32_t)kph, abortp, errp, PA_ERR_K_FULL);
           }
         }
       }
