@@ -45,32 +45,36 @@ __device__ int g_prompt_attn_err = 0;
 
 namespace {
 
-constexpr int PA_THREADS = 320;
+constexpr int PA_THREADS = 352;
 constexpr int PA_PROD_WARP = 8;
 constexpr int PA_MMA_WARP = 9;
-constexpr int PA_TILE = 128;
-constexpr int PA_SLOTS = 5;
-constexpr int PA_TILE_BYTES = PA_TILE * 256;     // 32 KB: a Q, K or V tile
+constexpr int PA_ROWS = 128;                     // rows of a Q tile
+constexpr int PA_KEYS = 64;                      // keys of a K or V tile
+constexpr int PA_SLOTS = 10;
+constexpr int PA_Q_BYTES = PA_ROWS * 256;        // two halves of 64 dims
+constexpr int PA_KV_BYTES = PA_KEYS * 256;
+constexpr int PA_KV_HALF = PA_KEYS * 128;
 constexpr float PA_SUM_MAX = 1.8446744e19f;      // 2^64
 constexpr int PA_BUCKETS = 512;
 constexpr int PA_SCHED_THREADS = 1024;
 
 enum { PA_ERR_ITEM = 1, PA_ERR_Q_EMPTY, PA_ERR_EMPTY, PA_ERR_Q_FULL, PA_ERR_K_FULL, PA_ERR_V_FULL, PA_ERR_P_FULL,
-       PA_ERR_O_FREE, PA_ERR_S_FULL, PA_ERR_PV_HALF, PA_ERR_O_FULL, PA_ERR_SCAN, PA_ERR_FINAL };
+       PA_ERR_O_FREE, PA_ERR_S_FULL, PA_ERR_PV_DONE, PA_ERR_O_FULL, PA_ERR_SCAN, PA_ERR_FINAL };
 
 struct __align__(8) PaBars {
   uint64_t full[PA_SLOTS], empty[PA_SLOTS];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2][2], pv_half[2], o_full[2], o_free[2], scan[2];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // [Q tile][buffer]
+  uint64_t o_full[2], o_free[2], scan[2];
   uint64_t item_full[2], item_empty[2];
-  uint64_t final_bar;
+  uint64_t final_bar[2];
 };
 
 struct PaSmall {
   PaBars bars;
   int4 item[2];                                  // b, pair, key head; b = -1: no more
-  int bad_v[2][2];                               // [Q tile][parity]: the scanned V tile is not finite
-  int skip[2];                                   // [Q tile]: this P V is not the tensor cores'
+  int bad_v[2][2];                               // [Q tile][parity]: the last scan whose V tile was not finite
+  int skip[2][2];                                // [Q tile][buffer]: this P V is not the tensor cores'
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -112,8 +116,8 @@ __device__ __forceinline__ PaItem pa_item(const PaShape& sh, const int32_t* __re
     it.s[w] = it.e[w] = 0;
     const int last = tw + it.n[w] - 1 + it.off;  // the last token's last key
     if (it.n[w] > 0 && last >= 0) {
-      it.e[w] = last / PA_TILE + 1;
-      it.s[w] = sh.window > 0 ? max(0, tw + it.off - sh.window + 1) / PA_TILE : 0;
+      it.e[w] = last / PA_KEYS + 1;
+      it.s[w] = sh.window > 0 ? max(0, tw + it.off - sh.window + 1) / PA_KEYS : 0;
       it.jb = min(it.jb, it.s[w]);
       it.je = max(it.je, it.e[w]);
     }
@@ -188,7 +192,7 @@ __global__ void __launch_bounds__(PA_SCHED_THREADS) prompt_schedule_kernel(PaSha
     int q0, nq, k0, nk;
     pa_seq(sh, cu_q, cu_k, b, q0, nq, k0, nk);
     sum += pa_pairs(sh, nq);
-    most = max(most, (nk + PA_TILE - 1) / PA_TILE);
+    most = max(most, (nk + PA_KEYS - 1) / PA_KEYS);
   }
   int incl = sum;
 #pragma unroll
@@ -214,7 +218,7 @@ __global__ void __launch_bounds__(PA_SCHED_THREADS) prompt_schedule_kernel(PaSha
   const int n = min(pa_before[sh.B], ws.cap);     // more only where cu_q is not ascending
   // bucket 0: the most key tiles (with a window never more than the window and a pair's tokens span)
   int top = most_s;
-  if (sh.window > 0) top = min(top, (sh.window + 2 * sh.tpt) / PA_TILE + 2);
+  if (sh.window > 0) top = min(top, (sh.window + 2 * sh.tpt) / PA_KEYS + 2);
   auto pair_of = [&](int i, int& b, int& pair) {
     int lo = 0, hi = sh.B;
     while (hi - lo > 1) {
@@ -261,32 +265,33 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_s = smem;                                   // [2 tiles][2 halves][128][128 B]
-  uint8_t* ring = q_s + 2 * PA_TILE_BYTES;               // [SLOTS][2 halves][128][128 B]
-  PaSmall* sm = reinterpret_cast<PaSmall*>(ring + PA_SLOTS * PA_TILE_BYTES);
+  uint8_t* ring = q_s + 2 * PA_Q_BYTES;                  // [SLOTS][2 halves][64][128 B]
+  PaSmall* sm = reinterpret_cast<PaSmall*>(ring + PA_SLOTS * PA_KV_BYTES);
   PaBars& bars = sm->bars;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows = sh.tpt * sh.G;                        // rows of a Q tile that hold a (token, head)
 
   if (tid == 0) {
-    for (int s = 0; s < PA_SLOTS; ++s) { mbar_init(&bars.full[s], 1); mbar_init(&bars.empty[s], 1); }
-    mbar_init(&bars.q_full, 1); mbar_init(&bars.q_empty, 1);
+    for (int s = 0; s < PA_SLOTS; ++s) { mbar_init(&bars.full[s], 1); mbar_init(&bars.empty[s], 2); }
+    mbar_init(&bars.q_full, 1); mbar_init(&bars.q_empty, 2);
     for (int w = 0; w < 2; ++w) {
-      mbar_init(&bars.s_full[w], 1); mbar_init(&bars.p_full[w][0], 4); mbar_init(&bars.p_full[w][1], 4);
-      mbar_init(&bars.pv_half[w], 1); mbar_init(&bars.o_full[w], 1); mbar_init(&bars.o_free[w], 4); mbar_init(&bars.scan[w], 4);
-      mbar_init(&bars.item_full[w], 1); mbar_init(&bars.item_empty[w], 9);
-      sm->skip[w] = 0;
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bars.s_full[w][i], 1); mbar_init(&bars.p_full[w][i], 4); mbar_init(&bars.pv_done[w][i], 1);
+      }
+      mbar_init(&bars.o_full[w], 1); mbar_init(&bars.o_free[w], 4); mbar_init(&bars.scan[w], 4);
+      mbar_init(&bars.item_full[w], 1); mbar_init(&bars.item_empty[w], 10);
+      mbar_init(&bars.final_bar[w], 1);
       sm->bad_v[w][0] = sm->bad_v[w][1] = 0;
     }
-    mbar_init(&bars.final_bar, 1);
     sm->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == PA_MMA_WARP) tmem_alloc(&sm->tmem_base, 512);
   // rows of no (token, head) are never loaded: zeros, so that their scores are finite
-  if (rows < PA_TILE)
-    for (int i = tid; i < 4 * (PA_TILE - rows) * 8; i += PA_THREADS) {
-      const int part = i / ((PA_TILE - rows) * 8), r = i % ((PA_TILE - rows) * 8);
-      reinterpret_cast<uint4*>(q_s + part * (PA_TILE * 128) + rows * 128)[r] = make_uint4(0u, 0u, 0u, 0u);
+  if (rows < PA_ROWS)
+    for (int i = tid; i < 4 * (PA_ROWS - rows) * 8; i += PA_THREADS) {
+      const int part = i / ((PA_ROWS - rows) * 8), r = i % ((PA_ROWS - rows) * 8);
+      reinterpret_cast<uint4*>(q_s + part * (PA_ROWS * 128) + rows * 128)[r] = make_uint4(0u, 0u, 0u, 0u);
     }
   fence_proxy_async_smem();
   tc_fence_before();
@@ -318,10 +323,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         if (kv >= PA_SLOTS &&
             !mbar_wait(&bars.empty[s], (uint32_t)((kv / PA_SLOTS - 1) & 1), abortp, errp, PA_ERR_EMPTY))
           return false;
-        uint8_t* dst = ring + s * PA_TILE_BYTES;
-        mbar_arrive_expect_tx(&bars.full[s], PA_TILE_BYTES);
+        uint8_t* dst = ring + s * PA_KV_BYTES;
+        mbar_arrive_expect_tx(&bars.full[s], PA_KV_BYTES);
         tma_load_3d(dst, map, 0, hk, row, &bars.full[s]);
-        tma_load_3d(dst + PA_TILE * 128, map, 64, hk, row, &bars.full[s]);
+        tma_load_3d(dst + PA_KV_HALF, map, 64, hk, row, &bars.full[s]);
         ++kv;
         return true;
       };
@@ -353,19 +358,21 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         if (x.x < 0) break;
         const PaItem it = pa_item(sh, cu_q, cu_k, x.x, x.y);
         const int hk = x.z;
-        if (it.jb < it.je && !load_tile(&tm_k, hk, it.k0 + it.jb * PA_TILE)) break;
+        if (it.jb < it.je && !load_tile(&tm_k, hk, it.k0 + it.jb * PA_KEYS)) break;
         if (n >= 1 && !mbar_wait(&bars.q_empty, (uint32_t)((n - 1) & 1), abortp, errp, PA_ERR_Q_EMPTY)) break;
         q_loads = n + 1;
         mbar_arrive_expect_tx(&bars.q_full, (uint32_t)(4 * rows * 128));
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const int tok = it.q0 + it.t0 + w * sh.tpt;
-          tma_load_3d(q_s + w * PA_TILE_BYTES, &tm_q, 0, hk * sh.G, tok, &bars.q_full);
-          tma_load_3d(q_s + w * PA_TILE_BYTES + PA_TILE * 128, &tm_q, 64, hk * sh.G, tok, &bars.q_full);
+          tma_load_3d(q_s + w * PA_Q_BYTES, &tm_q, 0, hk * sh.G, tok, &bars.q_full);
+          tma_load_3d(q_s + w * PA_Q_BYTES + PA_ROWS * 128, &tm_q, 64, hk * sh.G, tok, &bars.q_full);
         }
+        // in the order of use: K0 K1 V0 K2 V1 ..
+        if (it.jb + 1 < it.je) ok = load_tile(&tm_k, hk, it.k0 + (it.jb + 1) * PA_KEYS);
         for (int j = it.jb; j < it.je && ok; ++j) {
-          if (j > it.jb) ok = load_tile(&tm_k, hk, it.k0 + j * PA_TILE);
-          if (ok) ok = load_tile(&tm_v, hk, it.k0 + j * PA_TILE);
+          ok = load_tile(&tm_v, hk, it.k0 + j * PA_KEYS);
+          if (ok && j + 2 < it.je) ok = load_tile(&tm_k, hk, it.k0 + (j + 2) * PA_KEYS);
         }
         if (!ok) break;
       }
@@ -377,104 +384,97 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       }
     }
     __syncwarp();
-  } else if (warp == PA_MMA_WARP) {
-    // ------------------------------------------------------------ MMA issuer
+  } else if (warp >= PA_MMA_WARP) {
+    // ------------------------------------------------- MMA issuer of Q tile w
     // The whole warp walks the loop and one elected lane issues: descriptors stay
     // in uniform registers (a lone thread took 77-88 cycles for a product of 64).
-    {
-      constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false);
-      constexpr uint32_t ID_O = idesc_bf16(128, 128, false, true);
-      // low words of the descriptors of Q tile 0 and ring slot 0; an offset of x bytes adds x / 16
-      const uint64_t d_kmaj = smem_desc_sw128(0, 16, 1024), d_mnmaj = smem_desc_sw128(0, PA_TILE * 128, 1024);
-      const uint32_t q0 = smem_u32(q_s) >> 4, r0 = smem_u32(ring) >> 4;
-      auto uni = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
-      int ks = 0, kph = 0;                               // ring slot and phase of the next K
-      auto step = [](int& slot, int& ph) { if (++slot == PA_SLOTS) { slot = 0; ph ^= 1; } };
-      int p_it[2] = {0, 0}, o_it[2] = {0, 0};            // P tiles taken, items with a tile
-      bool ok = true;
-      for (int n = 0; ok; ++n) {
-        if (!mbar_wait(&bars.item_full[n & 1], (uint32_t)((n >> 1) & 1), abortp, errp, PA_ERR_ITEM)) break;
-        const int4 x = sm->item[n & 1];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.item_empty[n & 1]);
-        if (x.x < 0) break;
-        PaItem it = pa_item(sh, cu_q, cu_k, x.x, x.y);
-#pragma unroll
-        for (int w = 0; w < 2; ++w) { it.s[w] = uni(it.s[w]); it.e[w] = uni(it.e[w]); }
-        const int jb = uni(it.jb), je = uni(it.je);
-        if (!mbar_wait(&bars.q_full, (uint32_t)(n & 1), abortp, errp, PA_ERR_Q_FULL)) break;
-        if (jb == je) {
-          if (elect_one()) mma_commit(&bars.q_empty);
-          continue;
-        }
-        // V_(j - 1), K_j and V_j, K_(j + 1) are waited for while the products issued last still run
-        int vs = 0;                                      // ring slot of V_(j - 1)
-        ok = mbar_wait(&bars.full[ks], (uint32_t)kph, abortp, errp, PA_ERR_K_FULL);
-        for (int j = jb; j <= je && ok; ++j) {
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (j > it.s[w] && j <= it.e[w]) {           // P_w V of tile j - 1, 64 keys at a time
-              const bool first = j - 1 == it.s[w];
-              if (first && o_it[w] > 0)
-                ok = ok && mbar_wait(&bars.o_free[w], (uint32_t)((o_it[w] - 1) & 1), abortp, errp, PA_ERR_O_FREE);
-              if (first) ++o_it[w];
-              const uint32_t lo = uni(r0 + vs * (PA_TILE_BYTES / 16));
-              bool mine = true;
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                ok = ok && mbar_wait(&bars.p_full[w][h], (uint32_t)(p_it[w] & 1), abortp, errp, PA_ERR_P_FULL);
-                if (!ok) break;
-                tc_fence_after();
-                if (h == 0) mine = !reinterpret_cast<volatile int*>(sm->skip)[w];
-                if (elect_one()) {
-                  if (mine) {
-#pragma unroll
-                    for (int k = 4 * h; k < 4 * h + 4; ++k)
-                      mma_bf16_ts(tmem + 256 + w * 128, tmem + w * 128 + k * 8, d_mnmaj | (lo + k * (2048 / 16)), ID_O,
-                                  (!first || k > 0) ? 1u : 0u);
-                  }
-                  if (h == 0) mma_commit(&bars.pv_half[w]);
-                  else if (j == it.e[w]) mma_commit(&bars.o_full[w]);
-                }
-                __syncwarp();
-              }
-              if (!ok) break;
-              ++p_it[w];
-            }
-            if (j >= it.s[w] && j < it.e[w]) {           // S_w of tile j
-              tc_fence_after();
-              const uint32_t la = q0 + w * (PA_TILE_BYTES / 16), lb = uni(r0 + ks * (PA_TILE_BYTES / 16));
-              if (elect_one()) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const uint32_t off = ((k >> 2) * (PA_TILE * 128) + (k & 3) * 32) / 16;
-                  mma_bf16(tmem + w * 128, d_kmaj | (la + off), d_kmaj | (lb + off), ID_S, k > 0 ? 1u : 0u);
-                }
-                mma_commit(&bars.s_full[w]);
-              }
-              __syncwarp();
-            }
-          }
-          if (!ok) break;
+    constexpr uint32_t ID_S = idesc_bf16(PA_ROWS, PA_KEYS, false, false);
+    constexpr uint32_t ID_O = idesc_bf16(PA_ROWS, 128, false, true);
+    const int w = warp - PA_MMA_WARP;
+    auto uni = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
+    // low words of the descriptors of the Q tile and ring slot 0; an offset of x bytes adds x / 16
+    const uint64_t d_kmaj = smem_desc_sw128(0, 16, 1024), d_mnmaj = smem_desc_sw128(0, PA_KV_HALF, 1024);
+    const uint32_t q0 = uni(smem_u32(q_s + w * PA_Q_BYTES) >> 4), r0 = smem_u32(ring) >> 4;
+    const uint32_t t_s = uni(tmem + w * 128), t_o = uni(tmem + 256 + w * 128);
+    int slot = 0, ph = 0;                                // the ring, in the order of use
+    int s_it = 0, p_it = 0, o_it = 0;                    // S and P tiles, items with a tile
+    bool ok = true;
+    // the slot's products are issued (or it is the other Q tile's alone): release it
+    auto release = [&]() {
+      if (elect_one()) mma_commit(&bars.empty[slot]);
+      __syncwarp();
+      if (++slot == PA_SLOTS) { slot = 0; ph ^= 1; }
+    };
+    for (int n = 0; ok; ++n) {
+      if (!mbar_wait(&bars.item_full[n & 1], (uint32_t)((n >> 1) & 1), abortp, errp, PA_ERR_ITEM)) break;
+      const int4 x = sm->item[n & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.item_empty[n & 1]);
+      if (x.x < 0) break;
+      const PaItem it = pa_item(sh, cu_q, cu_k, x.x, x.y);
+      const int js = uni(w == 0 ? it.s[0] : it.s[1]), je = uni(w == 0 ? it.e[0] : it.e[1]);
+      const int jb = uni(it.jb), jend = uni(it.je);
+      if (!mbar_wait(&bars.q_full, (uint32_t)(n & 1), abortp, errp, PA_ERR_Q_FULL)) break;
+      auto issue_s = [&](int j) {                        // over the scores whose P V was issued before
+        ok = ok && mbar_wait(&bars.full[slot], (uint32_t)ph, abortp, errp, PA_ERR_K_FULL);
+        if (!ok) return;
+        if (j >= js && j < je) {
+          tc_fence_after();
+          const uint32_t lb = uni(r0 + slot * (PA_KV_BYTES / 16)), d = uni(t_s + (s_it & 1) * 64);
           if (elect_one()) {
-            if (j > jb) mma_commit(&bars.empty[vs]);
-            if (j < je) mma_commit(&bars.empty[ks]);
-            if (j == je - 1) mma_commit(&bars.q_empty);  // every S of the item has read Q
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_bf16(d, d_kmaj | (q0 + ((k >> 2) * (PA_ROWS * 128) + (k & 3) * 32) / 16),
+                       d_kmaj | (lb + ((k >> 2) * PA_KV_HALF + (k & 3) * 32) / 16), ID_S, k > 0 ? 1u : 0u);
+            mma_commit(&bars.s_full[w][s_it & 1]);
           }
           __syncwarp();
-          if (j < je) {                                  // the V behind this K, then the next K
-            step(ks, kph);
-            vs = ks;
-            ok = mbar_wait(&bars.full[ks], (uint32_t)kph, abortp, errp, PA_ERR_V_FULL);
-            step(ks, kph);
-            if (j + 1 < je) ok = ok && mbar_wait(&bars.full[ks], (uint32_t)kph, abortp, errp, PA_ERR_K_FULL);
-          }
+          ++s_it;
         }
+        release();
+        if (j == jend - 1) {                             // every S of the item has read Q
+          if (elect_one()) mma_commit(&bars.q_empty);
+          __syncwarp();
+        }
+      };
+      if (jb == jend) {
+        if (elect_one()) mma_commit(&bars.q_empty);
+        __syncwarp();
       }
-      if (elect_one()) mma_commit(&bars.final_bar);
-      __syncwarp();
-      mbar_wait_done(&bars.final_bar, 0, errp, PA_ERR_FINAL);   // also after an abort: the products finish on their own
+      for (int j = jb; j < min(jb + 2, jend); ++j) issue_s(j);
+      for (int j = jb; j < jend && ok; ++j) {
+        ok = mbar_wait(&bars.full[slot], (uint32_t)ph, abortp, errp, PA_ERR_V_FULL);
+        if (j >= js && j < je) {
+          const bool first = j == js;
+          const int b = p_it & 1;
+          if (first && o_it > 0)
+            ok = ok && mbar_wait(&bars.o_free[w], (uint32_t)((o_it - 1) & 1), abortp, errp, PA_ERR_O_FREE);
+          if (first) ++o_it;
+          const uint32_t lo = uni(r0 + slot * (PA_KV_BYTES / 16)), a = uni(t_s + b * 64);
+          ok = ok && mbar_wait(&bars.p_full[w][b], (uint32_t)((p_it >> 1) & 1), abortp, errp, PA_ERR_P_FULL);
+          if (!ok) break;
+          ++p_it;
+          tc_fence_after();
+          const bool mine = !reinterpret_cast<volatile int*>(sm->skip[w])[b];
+          if (elect_one()) {
+            if (mine) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_bf16_ts(t_o, a + k * 8, d_mnmaj | (lo + k * (2048 / 16)), ID_O, (!first || k > 0) ? 1u : 0u);
+            }
+            mma_commit(&bars.pv_done[w][b]);
+            if (j == je - 1) mma_commit(&bars.o_full[w]);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        release();
+        if (j + 2 < jend) issue_s(j + 2);
+      }
     }
+    if (elect_one()) mma_commit(&bars.final_bar[w]);
+    __syncwarp();
+    mbar_wait_done(&bars.final_bar[w], 0, errp, PA_ERR_FINAL);   // also after an abort: the products finish on their own
     __syncwarp();
   } else {
     // ------------------------------------------------------ softmax + epilogue
@@ -491,37 +491,36 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       y = __shfl_sync(0xffffffffu, (int)y, 0) != 0;
       return y;
     };
-    // is the V tile at ring position vv finite (slow = false)? thread = key; all four warps agree
+    // is the V tile at ring position vv finite (slow = false)? two threads to a key; all four warps agree
     auto scan_v = [&](int vv, bool& slow) -> bool {
-      const int vs = vv % PA_SLOTS;
-      const uint8_t* v_s = ring + vs * PA_TILE_BYTES;
+      const int vs = vv % PA_SLOTS, key = row >> 1;
+      const uint8_t* v_s = ring + vs * PA_KV_BYTES + (row & 1) * PA_KV_HALF + key * 128;
       if (!wait(&bars.full[vs], (uint32_t)((vv / PA_SLOTS) & 1), PA_ERR_V_FULL)) return false;
       __syncwarp();
       uint32_t bad = 0u;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const uint4 u = *reinterpret_cast<const uint4*>(v_s + (k >> 3) * (PA_TILE * 128) + row * 128 + (((k & 7) ^ (row & 7)) << 4));
+      for (int k = 0; k < 8; ++k) {
+        const uint4 u = *reinterpret_cast<const uint4*>(v_s + ((k ^ (key & 7)) << 4));
         const uint32_t u4[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)                      // an exponent of all ones
           bad |= (uint32_t)((u4[i] & 0x7f80u) == 0x7f80u) | (uint32_t)((u4[i] & 0x7f800000u) == 0x7f800000u);
       }
+      // the flag holds the number of the scan: a scan of the same parity only begins when all four
+      // warps have read this one's
       volatile int* flag = &sm->bad_v[w][scans & 1];
-      if (__any_sync(0xffffffffu, bad != 0u) && lane == 0) *flag = 1;
+      if (__any_sync(0xffffffffu, bad != 0u) && lane == 0) *flag = scans + 1;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.scan[w]);
       if (!wait(&bars.scan[w], (uint32_t)(scans & 1), PA_ERR_SCAN)) return false;
       __syncwarp();
-      slow = *flag != 0;
-      // the other parity's flag was read by everyone before this scan's arrivals, and the next
-      // scan waits for a tile that needs this warp
-      if (lane == 0 && (warp & 3) == 0) sm->bad_v[w][(scans + 1) & 1] = 0;
+      slow = *flag == scans + 1;
       ++scans;
       return true;
     };
-    // O += P V on the CUDA cores, entries with P = 0 left out; the tensor cores' products are done
-    auto slow_pv = [&](int vv, bool first) {
-      const uint8_t* v_s = ring + (vv % PA_SLOTS) * PA_TILE_BYTES;
+    // O += P V on the CUDA cores, entries with P = 0 left out; the products into O are done
+    auto slow_pv = [&](uint32_t t_p, int vv, bool first) {
+      const uint8_t* v_s = ring + (vv % PA_SLOTS) * PA_KV_BYTES;
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {                      // 32 dims at a time
         uint32_t r[32];
@@ -533,11 +532,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
           for (int i = 0; i < 32; ++i) r[i] = 0u;
         }
 #pragma unroll 1
-        for (int key = 0; key < PA_TILE; ++key) {
-          const uint32_t p2 = tmem_ld1(t_s + (key >> 1));
+        for (int key = 0; key < PA_KEYS; ++key) {
+          const uint32_t p2 = tmem_ld1(t_p + (key >> 1));
           tmem_wait_ld();
           const float p = (key & 1) ? bf16_hi(p2) : bf16_lo(p2);
-          const uint8_t* vr = v_s + (k >> 1) * (PA_TILE * 128);
+          const uint8_t* vr = v_s + (k >> 1) * PA_KV_HALF;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint4 u = *reinterpret_cast<const uint4*>(vr + sw128(key, (k & 1) * 4 + q));
@@ -572,27 +571,27 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       const int last_lo = sh.window > 0 ? max(0, tw + it.n[w] - 1 + it.off - sh.window + 1) : 0;
       float m = -INFINITY, l = 0.f;
       for (int j = it.s[w]; j < it.e[w]; ++j, ++t_it) {
-        const int base = j * PA_TILE;
+        const int base = j * PA_KEYS, b = t_it & 1;
+        const uint32_t t_p = t_s + b * 64;               // the tile's scores, then its P
         // masked for some token of the Q tile
-        const bool part = base + PA_TILE - 1 > first_last || base < last_lo;
-        const int hi = part && row_ok ? last + 1 - base : PA_TILE, l0 = part && row_ok ? lo - base : 0;
+        const bool part = base + PA_KEYS - 1 > first_last || base < last_lo;
+        const int hi = part && row_ok ? last + 1 - base : PA_KEYS, l0 = part && row_ok ? lo - base : 0;
+        // ring position of its V: behind the K of up to two tiles more
+        const int vv = kv0 + (j - it.jb) + min(j - it.jb + 2, it.je - it.jb);
         bool slow = false;
-        if (part && !scan_v(kv0 + 2 * (j - it.jb) + 1, slow)) { ok = false; break; }
-        // s_full(j) also says that every product before S_w(j) is done, PV_w(j - 1) among them
-        if (!wait(&bars.s_full[w], (uint32_t)(t_it & 1), PA_ERR_S_FULL)) { ok = false; break; }
+        if (!wait(&bars.s_full[w][b], (uint32_t)((t_it >> 1) & 1), PA_ERR_S_FULL)) { ok = false; break; }
+        // only now: the tile's scores say that the ring is less than a turn before its V
+        if (part && !scan_v(vv, slow)) { ok = false; break; }
         tc_fence_after();
         uint32_t s[2][32];
         auto at = [&](int k) { return __uint_as_float(s[k >> 5][k & 31]); };
-        auto load = [&](int h) {                         // the scores of 64 keys, masked
-          tmem_ld32(t_s + 64 * h, s[0]);
-          tmem_ld32(t_s + 64 * h + 32, s[1]);
-          tmem_wait_ld64(s);
-          if (part) {
+        tmem_ld32(t_p, s[0]);
+        tmem_ld32(t_p + 32, s[1]);
+        tmem_wait_ld64(s);
+        if (part) {
 #pragma unroll
-            for (int k = 0; k < 64; ++k)
-              s[k >> 5][k & 31] = 64 * h + k < hi && 64 * h + k >= l0 ? s[k >> 5][k & 31] : 0xff800000u;
-          }
-        };
+          for (int k = 0; k < 64; ++k) s[k >> 5][k & 31] = k < hi && k >= l0 ? s[k >> 5][k & 31] : 0xff800000u;
+        }
         auto row_max = [&]() -> float {
           float mx[4];
 #pragma unroll
@@ -601,81 +600,62 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
           for (int k = 4; k < 64; ++k) mx[k & 3] = fmaxf(mx[k & 3], at(k));
           return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         };
-        auto rescale = [&](float mx) {                   // to the reference mx >= m
-          const float alpha = mx > m ? ex2_approx((m - mx) * c) : 1.f;
-          m = fmaxf(m, mx);
-          l *= alpha;
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            uint32_t r[32];
-            tmem_ld32(t_o + k * 32, r);
-            tmem_wait_ld();
+        if (m == -INFINITY) m = row_max();               // the row's first visible keys set the reference
+        // P = 2^(c (s - m)) as bf16, two to a column, over the scores
+        const float neg = m == -INFINITY ? 0.f : -m * c;
+        float2 ps[4];
+        uint32_t pk[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-            tmem_st32(t_o + k * 32, r);
-          }
-        };
-        if (slow) {                                      // the whole tile's maximum first: no redo later
-          load(0);
-          float mx = row_max();
-          load(1);
-          mx = fmaxf(mx, row_max());
-          if (m == -INFINITY) m = mx;
-          if (j > it.s[w]) rescale(mx);
+        for (int k = 0; k < 4; ++k) ps[k] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          float2 a = fma2(make_float2(at(2 * k), at(2 * k + 1)), make_float2(c, c), make_float2(neg, neg));
+          a = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+          ps[k & 3] = add2(ps[k & 3], a);
+          pk[k] = pack_bf16x2(a.x, a.y);
         }
+        ps[0] = add2(add2(ps[0], ps[1]), add2(ps[2], ps[3]));
+        float sum = ps[0].x + ps[0].y;
+        // a stale reference (the probabilities leave the range), or c m does: the warp redoes the tile
+        const bool over = !(sum <= PA_SUM_MAX), far = fabsf(neg) > 1e30f;
+        const bool redo = __any_sync(0xffffffffu, over || far);
+        if ((redo || slow) && j > it.s[w]) {             // the products into O are done?
+          if (!wait(&bars.pv_done[w][b ^ 1], (uint32_t)(((t_it - 1) >> 1) & 1), PA_ERR_PV_DONE)) { ok = false; break; }
+          tc_fence_after();
+        }
+        if (redo) {
+          const float mx = over ? fmaxf(row_max(), m) : m;
+          const float alpha = mx > m ? ex2_approx((m - mx) * c) : 1.f;
+          m = mx;
+          l *= alpha;
+          if (j > it.s[w]) {
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              uint32_t r[32];
+              tmem_ld32(t_o + k * 32, r);
+              tmem_wait_ld();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          load(h);
-          if (m == -INFINITY) m = row_max();             // the row's first visible keys set the reference
-          // P = 2^(c (s - m)) as bf16, two to a column, over the scores that were read
-          const float neg = m == -INFINITY ? 0.f : -m * c;
-          float2 ps[4];
-          uint32_t pk[32];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) ps[k] = make_float2(0.f, 0.f);
+              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+              tmem_st32(t_o + k * 32, r);
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          sum = 0.f;
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            float2 a = fma2(make_float2(at(2 * k), at(2 * k + 1)), make_float2(c, c),
-                            make_float2(neg, neg));
-            a = make_float2(ex2_approx(a.x), ex2_approx(a.y));
-            ps[k & 3] = add2(ps[k & 3], a);
-            pk[k] = pack_bf16x2(a.x, a.y);
-          }
-          ps[0] = add2(add2(ps[0], ps[1]), add2(ps[2], ps[3]));
-          float sum = ps[0].x + ps[0].y;
-          // a stale reference (the probabilities leave the range), or c m does: the warp redoes these keys
-          const bool over = !(sum <= PA_SUM_MAX), far = fabsf(neg) > 1e30f;
-          if (__any_sync(0xffffffffu, over || far)) {
-            if (!slow && (h == 1 || j > it.s[w])) {
-              if (h == 1 && !wait(&bars.pv_half[w], (uint32_t)(t_it & 1), PA_ERR_PV_HALF)) { ok = false; break; }
-              tc_fence_after();
-              rescale(over ? row_max() : m);
-            } else if (over) {
-              m = fmaxf(m, row_max());
-            }
-            const float ref = m == -INFINITY ? 0.f : m;
-            sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float a = ex2_approx((at(2 * k) - ref) * c);
-              const float b = ex2_approx((at(2 * k + 1) - ref) * c);
-              sum += a + b;
-              pk[k] = pack_bf16x2(a, b);
-            }
-          }
-          l += sum;
-          tmem_st32(t_s + 32 * h, pk);
-          tmem_wait_st();
-          if (slow && h == 1) slow_pv(kv0 + 2 * (j - it.jb) + 1, j == it.s[w]);
-          if (lane == 0 && (warp & 3) == 0) sm->skip[w] = slow;
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0 && (!slow || h == 1)) {
-            if (slow) mbar_arrive(&bars.p_full[w][0]);
-            mbar_arrive(&bars.p_full[w][h]);
+            const float e0 = ex2_approx((at(2 * k) - ref) * c), e1 = ex2_approx((at(2 * k + 1) - ref) * c);
+            sum += e0 + e1;
+            pk[k] = pack_bf16x2(e0, e1);
           }
         }
-        if (!ok) break;
+        l += sum;
+        tmem_st32(t_p, pk);
+        tmem_wait_st();
+        if (slow) slow_pv(t_p, vv, j == it.s[w]);
+        if (lane == 0 && (warp & 3) == 0) sm->skip[w][b] = slow;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[w][b]);
       }
       if (!ok) break;
       kv0 += 2 * (it.je - it.jb);
@@ -732,7 +712,7 @@ long long pa_most_pairs(int B, int Tq, int tpt) { return (long long)Tq / (2 * tp
 }  // namespace
 
 size_t prompt_attn_workspace_bytes(int B, int Tq, int H, int Hkv) {
-  return 16 + (size_t)pa_most_pairs(B, Tq, PA_TILE / (H / Hkv)) * sizeof(int2);
+  return 16 + (size_t)pa_most_pairs(B, Tq, PA_ROWS / (H / Hkv)) * sizeof(int2);
 }
 
 cslc_status launch_prompt_attn(const uint16_t* q, const uint16_t* k, const uint16_t* v, const int32_t* cu_q,
@@ -740,22 +720,22 @@ cslc_status launch_prompt_attn(const uint16_t* q, const uint16_t* k, const uint1
                                long long k_stride, long long v_stride, int window, float scale, uint16_t* out,
                                float* lse, void* wsp, cudaStream_t stream) {
   const char* fn = "cslc_prompt_attn";
-  const size_t smem = 1024 + (size_t)(2 + PA_SLOTS) * PA_TILE_BYTES + sizeof(PaSmall);
+  const size_t smem = 1024 + 2 * PA_Q_BYTES + (size_t)PA_SLOTS * PA_KV_BYTES + sizeof(PaSmall);
   int dev = 0, n_sm = 148;
   cudaError_t err = cudaGetDevice(&dev);
   if (err == cudaSuccess) err = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
   if (err == cudaSuccess)
     err = cudaFuncSetAttribute(prompt_attn_sm100_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return set_error(CSLC_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(err));
-  const int G = H / Hkv, tpt = PA_TILE / G;
+  const int G = H / Hkv, tpt = PA_ROWS / G;
   const long long items = pa_most_pairs(B, Tq, tpt) * Hkv;
   const PaShape sh{B, Tq, Tk, H, Hkv, G, tpt, window, scale, scale * kLog2e, items <= n_sm ? 1 : 0};
   CUtensorMap tm_q, tm_k, tm_v;
   // without keys no tile of them is loaded: the maps only have to be valid
   const bool keys = Tk > 0;
   if (!make_tmap_bf16_rows128(&tm_q, q, H, Tq, q_stride, G, tpt) ||
-      !make_tmap_bf16_rows128(&tm_k, keys ? k : q, keys ? Hkv : H, keys ? Tk : Tq, keys ? k_stride : q_stride, 1, PA_TILE) ||
-      !make_tmap_bf16_rows128(&tm_v, keys ? v : q, keys ? Hkv : H, keys ? Tk : Tq, keys ? v_stride : q_stride, 1, PA_TILE))
+      !make_tmap_bf16_rows128(&tm_k, keys ? k : q, keys ? Hkv : H, keys ? Tk : Tq, keys ? k_stride : q_stride, 1, PA_KEYS) ||
+      !make_tmap_bf16_rows128(&tm_v, keys ? v : q, keys ? Hkv : H, keys ? Tk : Tq, keys ? v_stride : q_stride, 1, PA_KEYS))
     return set_error(CSLC_ERR_CUDA, "%s: tensor map encoding failed", fn);
   PaWs ws;
   ws.head = static_cast<int*>(wsp);
