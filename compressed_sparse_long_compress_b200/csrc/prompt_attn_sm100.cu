@@ -13,15 +13,15 @@
 //                   first visible tile and moves only when a tile's
 //                   probabilities sum above 2^64 (O in TMEM is rescaled then),
 //                   so the steady state needs no maximum. P goes back to TMEM
-//                   as bf16 over the tile's own scores and is the A operand of
-//                   P V from there: no shared memory and no proxy fence.
-//   warp 8          producer: Q tiles, K and V tiles (TMA, 5-deep ring of 32 KB)
-//   warp 9          TMEM allocation and the MMA-issuing thread. Order of issue:
-//                   PV0(j-1) S0(j) PV1(j-1) S1(j): while one tile's softmax
-//                   runs, the products of the other fill the tensor pipe. S_w(j)
-//                   overwrites P_w(j-1), which the PV issued just before it
-//                   reads: products of one thread run in the order of issue.
-// TMEM: S0 S1 (P over them) O0 O1, 128 columns each.
+//                   as bf16 and is the A operand of P V from there: no shared
+//                   memory and no proxy fence.
+//   warp 8          producer: Q tiles, K and V tiles of 64 keys (TMA, 10-deep
+//                   ring of 16 KB)
+//   warps 9, 10     MMA issue for Q tile 0 and 1 (9 also allocates TMEM): S of
+//                   the next tile as soon as this tile's scores are in
+//                   registers, P V of this tile when P is there. So a softmax
+//                   waits for neither product in the steady state.
+// TMEM columns of a Q tile: S 64, P 2 x 32, O 128; both tiles fill the 512.
 //
 // Order of work. prompt_schedule_kernel sorts the Q-tile pairs of all sequences
 // by their number of key tiles, largest first; the CTAs draw tickets, so ragged
@@ -59,13 +59,13 @@ constexpr int PA_BUCKETS = 512;
 constexpr int PA_SCHED_THREADS = 1024;
 
 enum { PA_ERR_ITEM = 1, PA_ERR_Q_EMPTY, PA_ERR_EMPTY, PA_ERR_Q_FULL, PA_ERR_K_FULL, PA_ERR_V_FULL, PA_ERR_P_FULL,
-       PA_ERR_O_FREE, PA_ERR_S_FULL, PA_ERR_PV_DONE, PA_ERR_O_FULL, PA_ERR_SCAN, PA_ERR_FINAL };
+       PA_ERR_O_FREE, PA_ERR_S_FULL, PA_ERR_S_READ, PA_ERR_PV_DONE, PA_ERR_O_FULL, PA_ERR_SCAN, PA_ERR_FINAL };
 
 struct __align__(8) PaBars {
   uint64_t full[PA_SLOTS], empty[PA_SLOTS];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // [Q tile][buffer]
-  uint64_t o_full[2], o_free[2], scan[2];
+  uint64_t s_full[2], s_read[2], o_full[2], o_free[2], scan[2];   // by Q tile
+  uint64_t p_full[2][2], pv_done[2][2];          // [Q tile][buffer]
   uint64_t item_full[2], item_empty[2];
   uint64_t final_bar[2];
 };
@@ -276,8 +276,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
     mbar_init(&bars.q_full, 1); mbar_init(&bars.q_empty, 2);
     for (int w = 0; w < 2; ++w) {
       for (int i = 0; i < 2; ++i) {
-        mbar_init(&bars.s_full[w][i], 1); mbar_init(&bars.p_full[w][i], 4); mbar_init(&bars.pv_done[w][i], 1);
+        mbar_init(&bars.p_full[w][i], 4); mbar_init(&bars.pv_done[w][i], 1);
       }
+      mbar_init(&bars.s_full[w], 1); mbar_init(&bars.s_read[w], 4);
       mbar_init(&bars.o_full[w], 1); mbar_init(&bars.o_free[w], 4); mbar_init(&bars.scan[w], 4);
       mbar_init(&bars.item_full[w], 1); mbar_init(&bars.item_empty[w], 10);
       mbar_init(&bars.final_bar[w], 1);
@@ -415,18 +416,20 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       const int js = uni(w == 0 ? it.s[0] : it.s[1]), je = uni(w == 0 ? it.e[0] : it.e[1]);
       const int jb = uni(it.jb), jend = uni(it.je);
       if (!mbar_wait(&bars.q_full, (uint32_t)(n & 1), abortp, errp, PA_ERR_Q_FULL)) break;
-      auto issue_s = [&](int j) {                        // over the scores whose P V was issued before
+      auto issue_s = [&](int j) {
         ok = ok && mbar_wait(&bars.full[slot], (uint32_t)ph, abortp, errp, PA_ERR_K_FULL);
+        if (ok && j >= js && j < je && s_it > 0)         // the last scores are in registers
+          ok = mbar_wait(&bars.s_read[w], (uint32_t)((s_it - 1) & 1), abortp, errp, PA_ERR_S_READ);
         if (!ok) return;
         if (j >= js && j < je) {
           tc_fence_after();
-          const uint32_t lb = uni(r0 + slot * (PA_KV_BYTES / 16)), d = uni(t_s + (s_it & 1) * 64);
+          const uint32_t lb = uni(r0 + slot * (PA_KV_BYTES / 16));
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma_bf16(d, d_kmaj | (q0 + ((k >> 2) * (PA_ROWS * 128) + (k & 3) * 32) / 16),
+              mma_bf16(t_s, d_kmaj | (q0 + ((k >> 2) * (PA_ROWS * 128) + (k & 3) * 32) / 16),
                        d_kmaj | (lb + ((k >> 2) * PA_KV_HALF + (k & 3) * 32) / 16), ID_S, k > 0 ? 1u : 0u);
-            mma_commit(&bars.s_full[w][s_it & 1]);
+            mma_commit(&bars.s_full[w]);
           }
           __syncwarp();
           ++s_it;
@@ -441,16 +444,17 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         if (elect_one()) mma_commit(&bars.q_empty);
         __syncwarp();
       }
-      for (int j = jb; j < min(jb + 2, jend); ++j) issue_s(j);
+      if (jb < jend) issue_s(jb);
       for (int j = jb; j < jend && ok; ++j) {
-        ok = mbar_wait(&bars.full[slot], (uint32_t)ph, abortp, errp, PA_ERR_V_FULL);
+        if (j + 1 < jend) issue_s(j + 1);
+        ok = ok && mbar_wait(&bars.full[slot], (uint32_t)ph, abortp, errp, PA_ERR_V_FULL);
         if (j >= js && j < je) {
           const bool first = j == js;
           const int b = p_it & 1;
           if (first && o_it > 0)
             ok = ok && mbar_wait(&bars.o_free[w], (uint32_t)((o_it - 1) & 1), abortp, errp, PA_ERR_O_FREE);
           if (first) ++o_it;
-          const uint32_t lo = uni(r0 + slot * (PA_KV_BYTES / 16)), a = uni(t_s + b * 64);
+          const uint32_t lo = uni(r0 + slot * (PA_KV_BYTES / 16)), a = uni(t_s + 64 + b * 32);
           ok = ok && mbar_wait(&bars.p_full[w][b], (uint32_t)((p_it >> 1) & 1), abortp, errp, PA_ERR_P_FULL);
           if (!ok) break;
           ++p_it;
@@ -469,7 +473,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         }
         if (!ok) break;
         release();
-        if (j + 2 < jend) issue_s(j + 2);
       }
     }
     if (elect_one()) mma_commit(&bars.final_bar[w]);
@@ -486,10 +489,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
     int kv0 = 0, t_it = 0, scans = 0, o_it = 0;          // ring position, this Q tile's key tiles, scans, items
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity, int code) -> bool {
-      bool y = true;
-      if (lane == 0) y = mbar_wait(bar, parity, abortp, errp, code);
-      y = __shfl_sync(0xffffffffu, (int)y, 0) != 0;
-      return y;
+      if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abortp, errp, code));
     };
     // is the V tile at ring position vv finite (slow = false)? two threads to a key; all four warps agree
     auto scan_v = [&](int vv, bool& slow) -> bool {
@@ -567,28 +568,34 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       const bool row_ok = ti < it.n[w];
       const int last = tok + it.off;                     // its last key (below 0: none) and first
       const int lo = sh.window > 0 ? max(0, last - sh.window + 1) : 0;
-      const int first_last = tw + it.off;                // the tile's first token's last key
-      const int last_lo = sh.window > 0 ? max(0, tw + it.n[w] - 1 + it.off - sh.window + 1) : 0;
+      // tiles masked for no token of the Q tile: [whole0, whole1)
+      const int whole0 = sh.window > 0 ? (max(0, tw + it.n[w] - 1 + it.off - sh.window + 1) + PA_KEYS - 1) / PA_KEYS : 0;
+      const int whole1 = (tw + it.off + 1) / PA_KEYS;
+      bool far = false;                                  // c m leaves fp32's range for a row of the warp
       float m = -INFINITY, l = 0.f;
       for (int j = it.s[w]; j < it.e[w]; ++j, ++t_it) {
-        const int base = j * PA_KEYS, b = t_it & 1;
-        const uint32_t t_p = t_s + b * 64;               // the tile's scores, then its P
-        // masked for some token of the Q tile
-        const bool part = base + PA_KEYS - 1 > first_last || base < last_lo;
-        const int hi = part && row_ok ? last + 1 - base : PA_KEYS, l0 = part && row_ok ? lo - base : 0;
+        const int b = t_it & 1;
+        const uint32_t t_p = t_s + 64 + b * 32;
+        const bool part = j < whole0 || j >= whole1;
         // ring position of its V: behind the K of up to two tiles more
         const int vv = kv0 + (j - it.jb) + min(j - it.jb + 2, it.je - it.jb);
         bool slow = false;
-        if (!wait(&bars.s_full[w][b], (uint32_t)((t_it >> 1) & 1), PA_ERR_S_FULL)) { ok = false; break; }
+        if (!wait(&bars.s_full[w], (uint32_t)(t_it & 1), PA_ERR_S_FULL)) { ok = false; break; }
+        // (the PV of two tiles before, which read this tile's P buffer, was issued before these
+        // scores, so it is done too)
         // only now: the tile's scores say that the ring is less than a turn before its V
         if (part && !scan_v(vv, slow)) { ok = false; break; }
         tc_fence_after();
         uint32_t s[2][32];
         auto at = [&](int k) { return __uint_as_float(s[k >> 5][k & 31]); };
-        tmem_ld32(t_p, s[0]);
-        tmem_ld32(t_p + 32, s[1]);
+        tmem_ld32(t_s, s[0]);
+        tmem_ld32(t_s + 32, s[1]);
         tmem_wait_ld64(s);
-        if (part) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.s_read[w]);
+        if (part && row_ok) {
+          const int hi = last + 1 - j * PA_KEYS, l0 = lo - j * PA_KEYS;
 #pragma unroll
           for (int k = 0; k < 64; ++k) s[k >> 5][k & 31] = k < hi && k >= l0 ? s[k >> 5][k & 31] : 0xff800000u;
         }
@@ -600,8 +607,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
           for (int k = 4; k < 64; ++k) mx[k & 3] = fmaxf(mx[k & 3], at(k));
           return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         };
-        if (m == -INFINITY) m = row_max();               // the row's first visible keys set the reference
-        // P = 2^(c (s - m)) as bf16, two to a column, over the scores
+        if (__any_sync(0xffffffffu, m == -INFINITY)) {   // the row's first visible keys set the reference
+          if (m == -INFINITY) m = row_max();
+          far = __any_sync(0xffffffffu, fabsf(m * c) > 1e30f && m != -INFINITY);
+        }
+        // P = 2^(c (s - m)) as bf16, two to a column
         const float neg = m == -INFINITY ? 0.f : -m * c;
         float2 ps[4];
         uint32_t pk[32];
@@ -617,8 +627,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         ps[0] = add2(add2(ps[0], ps[1]), add2(ps[2], ps[3]));
         float sum = ps[0].x + ps[0].y;
         // a stale reference (the probabilities leave the range), or c m does: the warp redoes the tile
-        const bool over = !(sum <= PA_SUM_MAX), far = fabsf(neg) > 1e30f;
-        const bool redo = __any_sync(0xffffffffu, over || far);
+        const bool over = !(sum <= PA_SUM_MAX), redo = __any_sync(0xffffffffu, over) || far;
         if ((redo || slow) && j > it.s[w]) {             // the products into O are done?
           if (!wait(&bars.pv_done[w][b ^ 1], (uint32_t)(((t_it - 1) >> 1) & 1), PA_ERR_PV_DONE)) { ok = false; break; }
           tc_fence_after();
@@ -628,6 +637,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
           const float alpha = mx > m ? ex2_approx((m - mx) * c) : 1.f;
           m = mx;
           l *= alpha;
+          far = __any_sync(0xffffffffu, fabsf(m * c) > 1e30f && m != -INFINITY);
           if (j > it.s[w]) {
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
