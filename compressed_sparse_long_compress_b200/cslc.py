@@ -476,47 +476,71 @@ def decode_append(state: AppendState, c, z, pos, pos_bias, nope, rope, kv_scale,
 
 # ------------------------------------------- uncompressed attention, paged cache
 
-def _rows(t, dtype, name, device, shape):
-    """As _need for rows of heads [rows, heads, 128] that may lie apart: dense
-    within a row, any row stride that is a multiple of 8 elements. Returns the stride."""
+def _device(t, dtype, name) -> int:
+    """The index of the CUDA device that a call runs on: its first tensor's."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} is on {t.device}, expected a CUDA device, {device}")
-    if tuple(t.shape) != tuple(shape):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return t.get_device()
+
+
+def _at(t, dtype, name, dev, shape):
+    """As _need, on device `dev`. Returns the address. (One expression for what is
+    right: a small call is bound by the time that its checks take.)"""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == dev and t.shape == shape
+            and t.is_contiguous()):
+        _need(t, dtype, name, shape)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    return t.data_ptr()
+
+
+def _rows(t, dtype, name, dev, shape):
+    """As _at for rows of heads [rows, heads, 128] that may lie apart: dense within
+    a row, any row stride that is a multiple of 8 elements. Returns the address and
+    the row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected the CUDA device cuda:{dev}")
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     n, h, d = shape
-    if h * d and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+    st = t.stride()
+    if h * d and (st[2] != 1 or (h > 1 and st[1] != d)):
         raise ValueError(f"{name} must be dense within a row")
-    return t.stride(0) if n > 1 else h * d
+    return t.data_ptr(), st[0] if n > 1 else h * d
 
 
-def _at(t, dtype, name, device, shape=None):
-    """As _need, on the given device."""
-    _need(t, dtype, name, shape)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return t
-
-
-def _alloc(shape, dtype, device, stream):
+def _alloc(shape, dtype, dev, stream):
     """Memory for a call on `stream`: from that stream's pool, so that it is not
     reused by another stream's work while the call still runs."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _run_on(device, stream, fn, *args):
+def _run_on(dev, stream, fn, *args):
     """fn(*args, stream) with the tensors' device current."""
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if s.device != device:
-        raise ValueError(f"the stream is on {s.device}, the tensors on {device}")
-    with torch.cuda.device(device):
-        _check(fn(*args, ctypes.c_void_p(s.cuda_stream)))
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
+    else:
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, raw)
+    if st != 0:
+        _check(st)
 
 
 def page_plan(old_len, new_len, free_pages, block_table, page: int, n_pages: int, max_tokens: int | None = None,
@@ -526,10 +550,12 @@ def page_plan(old_len, new_len, free_pages, block_table, page: int, n_pages: int
     block_table [B, max_pages] is updated in place. Pass max_tokens (the most new
     tokens of a step) or slots [max_tokens]. Returns (slots, cu [B + 1], seq_len
     [B], status [2]: pages handed out, tokens without a page)."""
-    dev = block_table.device
+    dev = _device(block_table, I32, "block_table")
     B, max_pages = block_table.shape
-    _at(old_len, I32, "old_len", dev, (B,)); _at(new_len, I32, "new_len", dev, (B,))
-    _at(free_pages, I32, "free_pages", dev, (free_pages.numel(),)); _at(block_table, I32, "block_table", dev)
+    n_free = free_pages.numel()
+    p_old = _at(old_len, I32, "old_len", dev, (B,)); p_new = _at(new_len, I32, "new_len", dev, (B,))
+    p_free = _at(free_pages, I32, "free_pages", dev, (n_free,))
+    p_table = _at(block_table, I32, "block_table", dev, (B, max_pages))
     if slots is None:
         if max_tokens is None:
             raise ValueError("page_plan: give max_tokens or slots")
@@ -537,31 +563,33 @@ def page_plan(old_len, new_len, free_pages, block_table, page: int, n_pages: int
     cu = _alloc((B + 1,), I32, dev, stream) if cu is None else cu
     seq_len = _alloc((B,), I32, dev, stream) if seq_len is None else seq_len
     status = _alloc((2,), I32, dev, stream) if status is None else status
-    _at(slots, I32, "slots", dev, (slots.numel(),)); _at(cu, I32, "cu", dev, (B + 1,))
-    _at(seq_len, I32, "seq_len", dev, (B,)); _at(status, I32, "status", dev, (2,))
-    _run_on(dev, stream, LIB.cslc_page_plan, _ptr(old_len), _ptr(new_len), B, _ptr(free_pages), free_pages.numel(), page,
-            n_pages, max_pages, slots.numel(), _ptr(block_table), _ptr(slots), _ptr(cu), _ptr(seq_len), _ptr(status))
+    n_slots = slots.numel()
+    p_slots = _at(slots, I32, "slots", dev, (n_slots,)); p_cu = _at(cu, I32, "cu", dev, (B + 1,))
+    p_len = _at(seq_len, I32, "seq_len", dev, (B,)); p_status = _at(status, I32, "status", dev, (2,))
+    _run_on(dev, stream, LIB.cslc_page_plan, p_old, p_new, B, p_free, n_free, page, n_pages, max_pages, n_slots, p_table,
+            p_slots, p_cu, p_len, p_status)
     return slots, cu, seq_len, status
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale, device):
-    n_pages, Hkv, P, D = k_cache.shape
-    _at(k_cache, U8, "k_cache", device); _at(v_cache, U8, "v_cache", device, k_cache.shape)
-    _at(k_scale, F32, "k_scale", device, (n_pages, Hkv)); _at(v_scale, F32, "v_scale", device, (n_pages, Hkv))
-    return n_pages, Hkv, P, D
+def _cache(k_cache, v_cache, k_scale, v_scale, dev):
+    """Sizes and addresses of a paged cache."""
+    shape = k_cache.shape
+    n_pages, Hkv, P, D = shape
+    return (n_pages, Hkv, P, D, _at(k_cache, U8, "k_cache", dev, shape), _at(v_cache, U8, "v_cache", dev, shape),
+            _at(k_scale, F32, "k_scale", dev, (n_pages, Hkv)), _at(v_scale, F32, "v_scale", dev, (n_pages, Hkv)))
 
 
 def page_write_e4m3(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
     """Quantises k, v [T, H_kv, 128] bf16 (rows may lie apart) into their slots [T]
     of the paged cache, in place: caches [n_pages, H_kv, P, 128] uint8 e4m3 codes,
     scales [n_pages, H_kv] fp32 (see cslc_page_write_e4m3 in include/cslc.h)."""
-    dev = k_cache.device
-    n_pages, Hkv, P, D = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    dev = _device(k_cache, U8, "k_cache")
+    n_pages, Hkv, P, D, pkc, pvc, pks, pvs = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     T = slots.numel()
-    ks = _rows(k, BF16, "k", dev, (T, Hkv, D)); vs = _rows(v, BF16, "v", dev, (T, Hkv, D))
-    _at(slots, I32, "slots", dev, (T,))
-    _run_on(dev, stream, LIB.cslc_page_write_e4m3, _ptr(k), _ptr(v), _ptr(slots), T, Hkv, D, P, n_pages, ks, vs,
-            _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale))
+    pk, ks = _rows(k, BF16, "k", dev, (T, Hkv, D))
+    pv, vs = _rows(v, BF16, "v", dev, (T, Hkv, D))
+    _run_on(dev, stream, LIB.cslc_page_write_e4m3, pk, pv, _at(slots, I32, "slots", dev, (T,)), T, Hkv, D, P, n_pages, ks,
+            vs, pkc, pvc, pks, pvs)
 
 
 def prompt_attn_workspace_bytes(B: int, Tq: int, H: int, Hkv: int) -> int:
@@ -573,27 +601,28 @@ def prompt_attn(q, k, v, cu_q, cu_k, scale: float, window: int = 0, out=None, ls
     k, v [Tk, H_kv, 128] bf16 (rows may lie apart), cu_q, cu_k [B + 1] int32 (see
     cslc_prompt_attn in include/cslc.h). Rows of no sequence are left as they
     were. lse=True allocates it. Returns (out [Tq, H, 128], lse [Tq, H] or None)."""
-    dev = q.device
+    dev = _device(q, BF16, "q")
     Tq, H, D = q.shape
     Tk, Hkv = k.shape[:2]
     B = cu_q.numel() - 1
-    qs = _rows(q, BF16, "q", dev, (Tq, H, D))
-    ks = _rows(k, BF16, "k", dev, (Tk, Hkv, D)); vs = _rows(v, BF16, "v", dev, (Tk, Hkv, D))
     if B < 0:
         raise ValueError("cu_q must have B + 1 entries")
-    _at(cu_q, I32, "cu_q", dev, (B + 1,)); _at(cu_k, I32, "cu_k", dev, (B + 1,))
-    out = _alloc((Tq, H, D), BF16, dev, stream) if out is None else _at(out, BF16, "out", dev, (Tq, H, D))
+    pq, qs = _rows(q, BF16, "q", dev, (Tq, H, D))
+    pk, ks = _rows(k, BF16, "k", dev, (Tk, Hkv, D))
+    pv, vs = _rows(v, BF16, "v", dev, (Tk, Hkv, D))
+    p_cu_q = _at(cu_q, I32, "cu_q", dev, (B + 1,)); p_cu_k = _at(cu_k, I32, "cu_k", dev, (B + 1,))
+    if out is None:
+        out = _alloc((Tq, H, D), BF16, dev, stream)
+    po = _at(out, BF16, "out", dev, (Tq, H, D))
     if lse is True:
         lse = _alloc((Tq, H), F32, dev, stream)
-    if lse is not None:
-        _at(lse, F32, "lse", dev, (Tq, H))
-    nbytes = LIB.cslc_prompt_attn_workspace_bytes(B, Tq, H, Hkv)
-    if ws is None and nbytes:
+    pl = None if lse is None else _at(lse, F32, "lse", dev, (Tq, H))
+    if ws is None:
+        nbytes = LIB.cslc_prompt_attn_workspace_bytes(B, Tq, H, Hkv)
         ws = _alloc((nbytes,), U8, dev, stream)
-    if ws is not None:
-        _at(ws, U8, "ws", dev)
-    _run_on(dev, stream, LIB.cslc_prompt_attn, _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, H, Hkv, D,
-            qs, ks, vs, window, float(scale), _ptr(out), _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel())
+    n_ws = ws.numel()
+    _run_on(dev, stream, LIB.cslc_prompt_attn, pq, pk, pv, p_cu_q, p_cu_k, B, Tq, Tk, H, Hkv, D, qs, ks, vs, window, scale,
+            po, pl, _at(ws, U8, "ws", dev, (n_ws,)), n_ws)
     return out, lse
 
 
@@ -607,25 +636,24 @@ def page_decode_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
     apart), over the paged e4m3 cache (see cslc_page_decode_attn in
     include/cslc.h). lse=True allocates it. Returns (out [B, H, 128], lse [B, H]
     or None)."""
-    dev = q.device
+    dev = _device(q, BF16, "q")
     B, H, D = q.shape
-    n_pages, Hkv, P, Dc = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    n_pages, Hkv, P, Dc, pkc, pvc, pks, pvs = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     if Dc != D:
         raise ValueError(f"the cache holds rows of {Dc}, q of {D}")
-    qs = _rows(q, BF16, "q", dev, (B, H, D))
+    pq, qs = _rows(q, BF16, "q", dev, (B, H, D))
     max_pages = block_table.shape[1]
-    _at(block_table, I32, "block_table", dev, (B, max_pages)); _at(seq_len, I32, "seq_len", dev, (B,))
-    out = _alloc((B, H, D), BF16, dev, stream) if out is None else _at(out, BF16, "out", dev, (B, H, D))
+    p_table = _at(block_table, I32, "block_table", dev, (B, max_pages)); p_len = _at(seq_len, I32, "seq_len", dev, (B,))
+    if out is None:
+        out = _alloc((B, H, D), BF16, dev, stream)
+    po = _at(out, BF16, "out", dev, (B, H, D))
     if lse is True:
         lse = _alloc((B, H), F32, dev, stream)
-    if lse is not None:
-        _at(lse, F32, "lse", dev, (B, H))
-    nbytes = LIB.cslc_page_decode_workspace_bytes(B, H, Hkv)
-    if ws is None and nbytes:
+    pl = None if lse is None else _at(lse, F32, "lse", dev, (B, H))
+    if ws is None:
+        nbytes = LIB.cslc_page_decode_workspace_bytes(B, H, Hkv)
         ws = _alloc((nbytes,), U8, dev, stream)
-    if ws is not None:
-        _at(ws, U8, "ws", dev)
-    _run_on(dev, stream, LIB.cslc_page_decode_attn, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-            _ptr(block_table), _ptr(seq_len), B, H, Hkv, D, P, n_pages, max_pages, qs, window, float(scale), _ptr(out),
-            _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel())
+    n_ws = ws.numel()
+    _run_on(dev, stream, LIB.cslc_page_decode_attn, pq, pkc, pvc, pks, pvs, p_table, p_len, B, H, Hkv, D, P, n_pages,
+            max_pages, qs, window, scale, po, pl, _at(ws, U8, "ws", dev, (n_ws,)), n_ws)
     return out, lse
