@@ -182,9 +182,16 @@ __device__ __forceinline__ int scale_exponent(float amax) {
   return min(max(e, PW_EMIN), PW_EMAX);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a <= 3.402823466e38f ? a : 0.f;
+// The larger absolute values of two pairs of bf16 (a NaN loses), and the same without
+// infinities: a magnitude of 0x7f80 and more is no number.
+__device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t x) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(m), "r"(x & 0x7fff7fffu));
+  return r;
+}
+__device__ __forceinline__ uint32_t only_finite2(uint32_t x) {
+  const uint32_t a = x & 0x7fff7fffu;
+  return ((a & 0xffffu) < 0x7f80u ? a & 0xffffu : 0u) | (a < 0x7f800000u ? a & 0xffff0000u : 0u);
 }
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -202,7 +209,7 @@ __device__ __forceinline__ float4 from_e4m3x4(uint32_t v) {
 
 // Grid: windows of W tokens x (K and V of the heads), the latter fastest so that
 // neighbouring CTAs read neighbouring memory. A CTA takes the runs that begin in its window.
-__global__ void __launch_bounds__(PW_THREADS) page_write_kernel(
+__global__ void __launch_bounds__(PW_THREADS, 4) page_write_kernel(
     const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, const int32_t* __restrict__ slots, int T, int W,
     int Hkv, int page_log2, int n_pages, long long k_stride, long long v_stride, uint8_t* __restrict__ k_cache,
     uint8_t* __restrict__ v_cache, float* __restrict__ k_scale, float* __restrict__ v_scale) {
@@ -240,26 +247,24 @@ __global__ void __launch_bounds__(PW_THREADS) page_write_kernel(
   }
   __syncthreads();
 
-  for (int i = 0; i < W; ++i) {                          // uniform over the CTA
-    if (!((s_break[i >> 5] >> (i & 31)) & 1u)) continue;
+  auto next_break = [&](int t) {                         // the first one at or behind t (one is behind the last token)
+    int wd = t >> 5;
+    uint32_t m = s_break[wd] & (0xffffffffu << (t & 31));
+    while (m == 0u) m = s_break[++wd];
+    return wd * 32 + __ffs(m) - 1;
+  };
+  for (int i = next_break(0), end; i < W; i = end) {     // uniform over the CTA
+    end = next_break(i + 1);
     const int slot = s_slot[i + 1];
     if (slot < 0) continue;
-    // the run ends at the next break
-    int end = i + 1;
-    {
-      int wd = end >> 5;
-      uint32_t m = s_break[wd] & (0xffffffffu << (end & 31));
-      while (m == 0u) m = s_break[++wd];
-      end = wd * 32 + __ffs(m) - 1;
-    }
     const int len = end - i;                             // <= P: a run ends at its page's end
     const int pid = slot >> page_log2, o = slot & (P - 1);
     const size_t ps = (size_t)pid * Hkv + head;
     uint8_t* dst = cache + (ps << page_log2) * kD;
     const uint16_t* run = src + (long long)(w0 + i) * stride;
 
+    const float old_scale = o > 0 ? scale[ps] : 0.f;
     uint4 x[4][2];                                       // up to 4 pieces of 16 dims
-    float amax = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int c = tid + j * PW_THREADS;                // row c / 8, dims 16 (c mod 8) ..
@@ -271,15 +276,23 @@ __global__ void __launch_bounds__(PW_THREADS) page_write_kernel(
         x[j][0] = x[j][1] = make_uint4(0u, 0u, 0u, 0u);
       }
     }
+    uint32_t m2 = 0u;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t w4[4] = {x[j][h].x, x[j][h].y, x[j][h].z, x[j][h].w};
+      for (int h = 0; h < 2; ++h)
+        m2 = absmax2(absmax2(absmax2(absmax2(m2, x[j][h].x), x[j][h].y), x[j][h].z), x[j][h].w);
+    if (__any_sync(0xffffffffu, (m2 & 0xffffu) == 0x7f80u || (m2 >> 16) == 0x7f80u)) {   // an infinity: leave it out
+      m2 = 0u;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          amax = fmaxf(amax, fmaxf(finite_abs(bf16_lo(w4[q])), finite_abs(bf16_hi(w4[q]))));
-      }
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          m2 = absmax2(absmax2(m2, only_finite2(x[j][h].x)), only_finite2(x[j][h].y));
+          m2 = absmax2(absmax2(m2, only_finite2(x[j][h].z)), only_finite2(x[j][h].w));
+        }
+    }
+    float amax = fmaxf(bf16_lo(m2), bf16_hi(m2));
     amax = warp_max(amax);
     if (lane == 0) s_max[warp] = amax;
     __syncthreads();
@@ -288,7 +301,7 @@ __global__ void __launch_bounds__(PW_THREADS) page_write_kernel(
     for (int w = 1; w < PW_THREADS / 32; ++w) amax = fmaxf(amax, s_max[w]);
     int e = scale_exponent(amax);
     if (o > 0) {
-      const int e_old = scale_exponent(448.f * scale[ps]);   // the exponent of a stored power of two
+      const int e_old = scale_exponent(448.f * old_scale);   // the exponent of a stored power of two
       e = max(e, e_old);
       if (e > e_old) {
         const float f = pow2(max(e_old - e, -120));
