@@ -171,7 +171,7 @@ cslc_status launch_page_plan(const int32_t* old_len, const int32_t* new_len, int
 
 namespace {
 
-constexpr int PW_THREADS = 256;
+constexpr int PW_THREADS = 256;             // at most: 2 P threads, 4 pieces of 16 dims each, hold a page
 constexpr int PW_MAX_PAGE = 128;
 constexpr int PW_EMIN = -40, PW_EMAX = 60;   // exponents a page scale may have
 
@@ -211,23 +211,18 @@ __device__ __forceinline__ float4 from_e4m3x4(uint32_t v) {
 // neighbouring CTAs read neighbouring memory. A CTA takes the runs that begin in its window.
 __global__ void __launch_bounds__(PW_THREADS, 4) page_write_kernel(
     const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, const int32_t* __restrict__ slots, int T, int W,
-    int Hkv, int page_log2, int n_pages, long long k_stride, long long v_stride, uint8_t* __restrict__ k_cache,
+    int R, int Hkv, int page_log2, int n_pages, long long k_stride, long long v_stride, uint8_t* __restrict__ k_cache,
     uint8_t* __restrict__ v_cache, float* __restrict__ k_scale, float* __restrict__ v_scale) {
   __shared__ int s_slot[2 * PW_MAX_PAGE + 1];            // slots of tokens w0 - 1 .. w0 + W + P - 1
   __shared__ uint32_t s_break[2 * PW_MAX_PAGE / 32 + 1]; // bit t: token w0 + t does not continue a run
   __shared__ float s_max[PW_THREADS / 32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
   const int P = 1 << page_log2;
-  const int y = blockIdx.x % (2 * Hkv), w0 = blockIdx.x / (2 * Hkv) * W;
-  const bool is_v = y >= Hkv;
-  const int head = is_v ? y - Hkv : y;
-  const uint16_t* src = (is_v ? v : k) + head * kD;
-  const long long stride = is_v ? v_stride : k_stride;
-  uint8_t* cache = is_v ? v_cache : k_cache;
-  float* scale = is_v ? v_scale : k_scale;
+  const int groups = 2 * Hkv / R;                        // of R heads of K or V each
+  const int y0 = blockIdx.x % groups * R, w0 = blockIdx.x / groups * W;
 
-  const int n = W + P;                                   // <= 256
-  for (int i = tid; i < n + 1; i += PW_THREADS) {
+  const int n = W + P;                                   // at most 2 P
+  for (int i = tid; i < n + 1; i += threads) {
     const int t = w0 - 1 + i;
     int s = t >= 0 && t < T ? slots[t] : -1;
     if (s >= 0 && (s >> page_log2) >= n_pages) s = -1;
@@ -243,7 +238,7 @@ __global__ void __launch_bounds__(PW_THREADS, 4) page_write_kernel(
     }
     const uint32_t m = __ballot_sync(0xffffffffu, brk);
     if (lane == 0) s_break[warp] = m;
-    if (tid == 0) s_break[PW_THREADS / 32] = 0xffffffffu;
+    if (tid == 0) s_break[threads / 32] = 0xffffffffu;
   }
   __syncthreads();
 
@@ -259,6 +254,13 @@ __global__ void __launch_bounds__(PW_THREADS, 4) page_write_kernel(
     if (slot < 0) continue;
     const int len = end - i;                             // <= P: a run ends at its page's end
     const int pid = slot >> page_log2, o = slot & (P - 1);
+    for (int y = y0; y < y0 + R; ++y) {
+    const bool is_v = y >= Hkv;
+    const int head = is_v ? y - Hkv : y;
+    const uint16_t* src = (is_v ? v : k) + head * kD;
+    const long long stride = is_v ? v_stride : k_stride;
+    uint8_t* cache = is_v ? v_cache : k_cache;
+    float* scale = is_v ? v_scale : k_scale;
     const size_t ps = (size_t)pid * Hkv + head;
     uint8_t* dst = cache + (ps << page_log2) * kD;
     const uint16_t* run = src + (long long)(w0 + i) * stride;
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(PW_THREADS, 4) page_write_kernel(
     uint4 x[4][2];                                       // up to 4 pieces of 16 dims
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int c = tid + j * PW_THREADS;                // row c / 8, dims 16 (c mod 8) ..
+      const int c = tid + j * threads;                // row c / 8, dims 16 (c mod 8) ..
       if (c < len * 8) {
         const uint4* p = reinterpret_cast<const uint4*>(run + (long long)(c >> 3) * stride + (c & 7) * 16);
         x[j][0] = __ldcs(p);
@@ -296,16 +298,14 @@ __global__ void __launch_bounds__(PW_THREADS, 4) page_write_kernel(
     amax = warp_max(amax);
     if (lane == 0) s_max[warp] = amax;
     __syncthreads();
-    amax = s_max[0];
-#pragma unroll
-    for (int w = 1; w < PW_THREADS / 32; ++w) amax = fmaxf(amax, s_max[w]);
+    for (int w = 0; w < threads / 32; ++w) amax = fmaxf(amax, s_max[w]);
     int e = scale_exponent(amax);
     if (o > 0) {
       const int e_old = scale_exponent(448.f * old_scale);   // the exponent of a stored power of two
       e = max(e, e_old);
       if (e > e_old) {
         const float f = pow2(max(e_old - e, -120));
-        for (int c = tid; c < o * 8; c += PW_THREADS) {
+        for (int c = tid; c < o * 8; c += threads) {
           uint4* p = reinterpret_cast<uint4*>(dst + (size_t)c * 16);
           uint4 u = *p;
           uint32_t* w4 = reinterpret_cast<uint32_t*>(&u);
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(PW_THREADS, 4) page_write_kernel(
     const float inv = pow2(-e);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int c = tid + j * PW_THREADS;
+      const int c = tid + j * threads;
       if (c < len * 8) {
         uint4 u;
         uint32_t* w4 = reinterpret_cast<uint32_t*>(&u);
@@ -338,6 +338,7 @@ __global__ void __launch_bounds__(PW_THREADS, 4) page_write_kernel(
     }
     __syncthreads();                                     // every thread has read the old scale and s_max
     if (tid == 0) scale[ps] = pow2(e);
+    }
   }
 }
 
@@ -347,8 +348,11 @@ cslc_status launch_page_write(const uint16_t* k, const uint16_t* v, const int32_
   // a window of a page where that fills the GPU, of fewer tokens where it does not
   int W = page;
   while (W > 1 && (long long)((T + W - 1) / W) * 2 * Hkv < 4 * 148) W >>= 1;
-  const unsigned grid = (unsigned)((T + W - 1) / W) * 2u * (unsigned)Hkv;
-  page_write_kernel<<<grid, PW_THREADS, 0, stream>>>(k, v, slots, T, W, Hkv, 31 - __builtin_clz(page), n_pages, k_stride,
+  // several heads to a CTA, which then reads the slots once, while two rounds of CTAs remain
+  int R = 1;
+  while (R < 8 && (2 * Hkv) % (2 * R) == 0 && (long long)((T + W - 1) / W) * (2 * Hkv / (2 * R)) >= 8 * 148) R *= 2;
+  const unsigned grid = (unsigned)((T + W - 1) / W) * (unsigned)(2 * Hkv / R);
+  page_write_kernel<<<grid, page < 32 ? 64 : 2 * page, 0, stream>>>(k, v, slots, T, W, R, Hkv, 31 - __builtin_clz(page), n_pages, k_stride,
                                                      v_stride, k_cache, v_cache, k_scale, v_scale);
   return check_launch("page_write_kernel");
 }
