@@ -20,13 +20,15 @@
 // 2^-23 per token.
 //
 // Work. All tiles of all units, in the order of the sequences, are dealt to the
-// CTAs in equal consecutive ranges (two CTAs per SM), whatever the lengths are.
+// CTAs in equal consecutive ranges (two CTAs per SM), whatever the lengths are;
+// a unit counts PD_UNIT tiles more for its start and end.
 // A unit that crosses CTAs leaves fp32 partials in the workspace, which
 // page_decode_combine_kernel (a programmatic dependent launch) merges.
 //
 // CTA roles: warps 0-3 softmax (thread = token, then = dim), warp 4 producer
 // (page table and scales, one tile ahead; TMA of each page's codes, STAGES-deep
-// ring), warp 5 TMEM allocation and the MMA-issuing thread. Tokens outside
+// ring; the parts of q, a segment ahead), warp 5 TMEM allocation and the
+// MMA-issuing thread. Tokens outside
 // the sequence's visible range get P = 0 and their V rows are cleared in shared memory,
 // since stale codes may be NaN. All waits are time-bounded.
 
@@ -47,15 +49,20 @@ constexpr int PD_TILE = 128;
 constexpr int PD_STAGES = 3;
 constexpr int PD_HALF = PD_TILE * 128;        // 16 KB: K or V codes of a tile
 constexpr int PD_CTAS = 296;                  // two per SM on 148 SMs
+constexpr int PD_UNIT = 2;                    // what a unit costs besides its tiles, in tiles
 
-enum { PD_ERR_EMPTY = 1, PD_ERR_K_FULL, PD_ERR_V_FULL, PD_ERR_Q_FULL, PD_ERR_S_FULL, PD_ERR_P_FULL, PD_ERR_O_FULL,
+enum { PD_ERR_EMPTY = 1, PD_ERR_K_FULL, PD_ERR_V_FULL, PD_ERR_Q_FULL, PD_ERR_Q_EMPTY, PD_ERR_S_FULL, PD_ERR_P_FULL, PD_ERR_O_FULL,
        PD_ERR_FINAL };
 
 struct __align__(8) PdBars {
   uint64_t k_full[PD_STAGES], v_full[PD_STAGES], empty[PD_STAGES];
   uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t q_full, final_bar;
+  uint64_t q_full[2], q_empty[2], final_bar;
 };
+
+// Buffers of q's parts: two where two CTAs of an SM have the shared memory for it.
+template <int GP>
+constexpr int pd_qbufs() { return GP == 8 ? 2 : 1; }
 
 template <int GP>
 struct PdSmall {
@@ -63,10 +70,10 @@ struct PdSmall {
   float ks[PD_STAGES][8];                     // scale of each page of the tile's keys
   int ev[PD_STAGES][8];                       // exponent of its values' scale; PD_ABSENT: no such page
   __align__(16) float smax[2][GP][4];         // a tile's maxima by warp
-  float lsum[GP][4];
-  float qs[GP];                               // what a score of the parts' products is multiplied with
+  float lsum[2][GP][4];                       // by segment parity
+  float qs[pd_qbufs<GP>()][GP];                            // what a score of the parts' products is multiplied with
   long long scan[PD_THREADS / 32];
-  long long x_pre;                            // tiles before sequence x_b
+  long long x_pre;                            // work before sequence x_b
   int x_b;
   uint32_t tmem_base;
   int abort_flag;
@@ -94,26 +101,41 @@ __device__ __forceinline__ int pd_tiles(const PdShape& sh, const int32_t* __rest
   return (n + PD_TILE - 1) / PD_TILE - t0;
 }
 
-// Walks a CTA's range [x, x1) of the tiles, a segment (tiles of one unit) at a time.
+// Work of one unit of sequence b: its tiles and PD_UNIT, nothing without a tile.
+__device__ __forceinline__ int pd_work(const PdShape& sh, const int32_t* __restrict__ seq_len, int b) {
+  const int nt = pd_tiles(sh, seq_len, b);
+  return nt > 0 ? nt + PD_UNIT : 0;
+}
+
+// Walks a CTA's range [x, x1) of the work, a segment (tiles of one unit) at a
+// time. A unit's first PD_UNIT positions stand for its cost besides the tiles.
 struct PdWalk {
-  long long x, x1, pre;                       // pre: tiles before sequence b (over one unit each)
+  long long x, x1, pre;                       // pre: work before sequence b (over one unit each)
   int b;
   // the segment: tiles t .. t + len - 1 of the nt tiles of unit u of sequence b
   int u, t, len, nt;
   __device__ __forceinline__ bool next(const PdShape& sh, const int32_t* __restrict__ seq_len) {
     if (x >= x1) return false;
     const int HU = sh.Hkv * sh.HG;
+    int w;
     while (true) {
-      nt = pd_tiles(sh, seq_len, b);
-      if (x < (pre + nt) * HU) break;
-      pre += nt;
+      w = pd_work(sh, seq_len, b);
+      if (x < (pre + w) * HU) break;
+      pre += w;
       ++b;
     }
+    nt = w - PD_UNIT;
     const long long off = x - pre * HU;
-    u = (int)(off / nt);
-    t = (int)(off - (long long)u * nt);
-    len = (int)min((long long)(nt - t), x1 - x);
-    x += len;
+    u = (int)(off / w);
+    const int r = (int)(off - (long long)u * w), skip = max(0, PD_UNIT - r);
+    t = max(0, r - PD_UNIT);
+    const long long most = x1 - x - skip;
+    if (most <= 0) {                          // the range ends before the unit's first tile
+      x = x1;
+      return false;
+    }
+    len = (int)min((long long)(nt - t), most);
+    x += skip + len;
     return true;
   }
 };
@@ -123,7 +145,7 @@ struct PdWalk {
 // Partials in the workspace: per CTA a header of 8 ints, then per slot (two per
 // CTA: its first segment, its last one) GP x 128 sums and GP (reference, sum).
 struct PdWs {
-  int* hdr;       // [PD_CTAS][8]: b, u, t, nt, tiles per CTA (two words); b = -1 when no unit continues here
+  int* hdr;       // [PD_CTAS][8]: b, u, t, nt, work per CTA (two words); b = -1 when no unit continues here
   float* o;       // [2 PD_CTAS][GP][128]
   float2* rl;     // [2 PD_CTAS][GP]
 };
@@ -133,12 +155,12 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
     PdShape sh, const uint16_t* __restrict__ q, const float* __restrict__ k_scale, const float* __restrict__ v_scale,
     const int32_t* __restrict__ table, const int32_t* __restrict__ seq_len, uint16_t* __restrict__ out,
     float* __restrict__ lse, PdWs ws, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
-  constexpr int N = 2 * GP;
+  constexpr int N = 2 * GP, QB = pd_qbufs<GP>();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* kv_s = smem;                                   // [STAGES][K 16 KB | V 16 KB]
-  uint8_t* q_s = kv_s + PD_STAGES * 2 * PD_HALF;          // [N][128 B]
-  uint8_t* p_s = q_s + N * 128;                           // [2][N][128 B]
+  uint8_t* q_s = kv_s + PD_STAGES * 2 * PD_HALF;          // [QB][N][128 B]
+  uint8_t* p_s = q_s + QB * N * 128;                      // [2][N][128 B]
   PdSmall<GP>* sm = reinterpret_cast<PdSmall<GP>*>(p_s + 2 * N * 128);
   PdBars& bars = sm->bars;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -149,20 +171,20 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
       mbar_init(&bars.k_full[s], 1); mbar_init(&bars.v_full[s], 1); mbar_init(&bars.empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) { mbar_init(&bars.s_full[i], 1); mbar_init(&bars.p_full[i], 4); mbar_init(&bars.o_full[i], 1); }
-    mbar_init(&bars.q_full, 4);
+    for (int i = 0; i < 2; ++i) { mbar_init(&bars.q_full[i], 1); mbar_init(&bars.q_empty[i], 5); }
     mbar_init(&bars.final_bar, 1);
     sm->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == PD_MMA_WARP) tmem_alloc(&sm->tmem_base, 4 * N < 32 ? 32 : 4 * N);
 
-  // ---- this CTA's range of the tiles: a scan of the sequences' tile counts
+  // ---- this CTA's range of the work: a scan over the sequences
   long long x0, x1, per;
   {
     const int each = (sh.B + PD_THREADS - 1) / PD_THREADS;
     const int b0 = min(sh.B, tid * each), b1 = min(sh.B, b0 + each);
     long long sum = 0;
-    for (int b = b0; b < b1; ++b) sum += pd_tiles(sh, seq_len, b);
+    for (int b = b0; b < b1; ++b) sum += pd_work(sh, seq_len, b);
     long long incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -180,14 +202,14 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
     per = (total + gridDim.x - 1) / gridDim.x;
     x0 = min(total, per * blockIdx.x);
     x1 = min(total, x0 + per);
-    // the thread whose sequences hold tile x0 finds the sequence
+    // the thread whose sequences hold position x0 finds the sequence
     if (x0 < x1 && x0 >= (incl - sum) * HU && x0 < incl * HU) {
       long long pre = incl - sum;
       int b = b0;
       while (true) {
-        const int nt = pd_tiles(sh, seq_len, b);
-        if (x0 < (pre + nt) * HU) break;
-        pre += nt;
+        const int w = pd_work(sh, seq_len, b);
+        if (x0 < (pre + w) * HU) break;
+        pre += w;
         ++b;
       }
       sm->x_pre = pre;
@@ -209,9 +231,7 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
     const int P = 1 << sh.page_log2;
     if (lane == 0) { tma_prefetch_map(&tm_k); tma_prefetch_map(&tm_v); }
     int it = 0;
-    bool ok = true;
-    // lane i < ppt holds page i of the tile; the next tile's entry and scales
-    // are loaded before this tile's wait
+    // lane i < ppt holds page i of the tile
     auto load = [&](int b, int u, int lo, int n, int tile, int& y, float& ks, int& ev) {
       y = -1; ks = 0.f; ev = PD_ABSENT;
       if (lane < ppt) {
@@ -229,36 +249,100 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
         }
       }
     };
-    while (ok && walk.next(sh, seq_len)) {
-      int lo, t0;
-      const int n = pd_range(sh, seq_len, walk.b, lo, t0);
-      int y, ev;
-      float ks;
-      load(walk.b, walk.u, lo, n, t0 + walk.t, y, ks, ev);
-      for (int i = 0; i < walk.len; ++i, ++it) {
-        const int s = it % PD_STAGES;
-        int y2 = -1, ev2 = PD_ABSENT;
-        float ks2 = 0.f;
-        if (i + 1 < walk.len) load(walk.b, walk.u, lo, n, t0 + walk.t + i + 1, y2, ks2, ev2);
-        if (it >= PD_STAGES) {
-          bool w = true;
-          if (lane == 0) w = mbar_wait(&bars.empty[s], (uint32_t)((it / PD_STAGES - 1) & 1), abortp, errp, PD_ERR_EMPTY);
-          ok = __shfl_sync(0xffffffffu, (int)w, 0) != 0;
-          if (!ok) break;
-        }
-        if (lane < ppt) { sm->ks[s][lane] = ks; sm->ev[s][lane] = ev; }
-        __syncwarp();
-        if (lane == 0) { mbar_arrive_expect_tx(&bars.k_full[s], PD_HALF); mbar_arrive_expect_tx(&bars.v_full[s], PD_HALF); }
-        __syncwarp();
-        // a page that is not there reads the zero fill (a row past the end)
-        if (lane < ppt) {
-          const int row = y >= 0 ? y : max(1, (int)(((long long)sh.n_pages * sh.Hkv) << sh.page_log2));
-          uint8_t* dst = kv_s + s * 2 * PD_HALF + (lane << sh.page_log2) * 128;
-          tma_load_2d(dst, &tm_k, 0, row, &bars.k_full[s]);
-          tma_load_2d(dst + PD_HALF, &tm_v, 0, row, &bars.v_full[s]);
-        }
-        y = y2; ks = ks2; ev = ev2;
+    // q of a segment in two parts: lane = 4 dims, all heads' loads first
+    auto put_q = [&](int seg, int b, int u) -> bool {
+      const int qb = seg % QB;
+      const int hk = u / sh.HG, g0 = (u - hk * sh.HG) * GP, gc = min(GP, sh.G - g0);
+      uint2 v[GP];
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        v[g] = make_uint2(0u, 0u);
+        if (g < gc) v[g] = reinterpret_cast<const uint2*>(q + (long long)b * sh.q_stride + (long long)(hk * sh.G + g0 + g) * kD)[lane];
       }
+      bool w = true;
+      if (seg >= QB) {
+        if (lane == 0) w = mbar_wait(&bars.q_empty[qb], (uint32_t)((seg / QB - 1) & 1), abortp, errp, PD_ERR_Q_EMPTY);
+        w = __shfl_sync(0xffffffffu, (int)w, 0) != 0;
+        if (!w) return false;
+      }
+      uint8_t* dst = q_s + qb * N * 128;
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        const float f[4] = {bf16_lo(v[g].x), bf16_hi(v[g].x), bf16_lo(v[g].y), bf16_hi(v[g].y)};
+        float am = 0.f;
+        bool fin = true;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = fabsf(f[i]);
+          fin = fin && a <= 3.402823466e38f;
+          am = fmaxf(am, a <= 3.402823466e38f ? a : 0.f);
+        }
+        am = warp_redux_max(am);
+        fin = __all_sync(0xffffffffu, fin);
+        // am in [2^e, 2^(e+1)): times 2^(7 - e); the exponent is held where both powers are normal
+        const int e = max(-110, (int)(__float_as_uint(am) >> 23) - 127) - 7;
+        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+        uint32_t hi = 0u, lw = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float a = f[i] * inv, c = f[i + 1] * inv;
+          const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(a, c), __NV_SATFINITE, __NV_E4M3);
+          const float2 d = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2, __NV_E4M3)));
+          const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2((a - d.x) * 16.f, (c - d.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
+          hi |= h2 << (8 * i);
+          lw |= l2 << (8 * i);
+        }
+        *reinterpret_cast<uint32_t*>(dst + sw128(g, lane >> 2) + (lane & 3) * 4) = hi;
+        *reinterpret_cast<uint32_t*>(dst + sw128(GP + g, lane >> 2) + (lane & 3) * 4) = lw;
+        // a row of q that is not finite has no finite score
+        if (lane == 0) sm->qs[qb][g] = fin ? sh.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) : __int_as_float(0x7fc00000);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.q_full[qb]);
+      return true;
+    };
+    // the tiles of all segments in turn; a tile's page entries are loaded one tile ahead
+    int lo = 0, n = 0, t0 = 0, i = 0, seg = -1;
+    auto advance = [&]() -> bool {
+      if (seg >= 0 && ++i < walk.len) return true;
+      if (!walk.next(sh, seq_len)) return false;
+      n = pd_range(sh, seq_len, walk.b, lo, t0);
+      i = 0;
+      ++seg;
+      return true;
+    };
+    int y = -1, ev = PD_ABSENT;
+    float ks = 0.f;
+    bool more = advance();
+    if (more) load(walk.b, walk.u, lo, n, t0 + walk.t, y, ks, ev);
+    while (more) {
+      const int s = it % PD_STAGES;
+      const bool new_seg = i == 0;
+      const int seg_now = seg, b_now = walk.b, u_now = walk.u;
+      int y2 = -1, ev2 = PD_ABSENT;
+      float ks2 = 0.f;
+      more = advance();
+      if (more) load(walk.b, walk.u, lo, n, t0 + walk.t + i, y2, ks2, ev2);
+      if (it >= PD_STAGES) {
+        bool w = true;
+        if (lane == 0) w = mbar_wait(&bars.empty[s], (uint32_t)((it / PD_STAGES - 1) & 1), abortp, errp, PD_ERR_EMPTY);
+        if (!__shfl_sync(0xffffffffu, (int)w, 0)) break;
+      }
+      if (lane < ppt) { sm->ks[s][lane] = ks; sm->ev[s][lane] = ev; }
+      __syncwarp();
+      if (lane == 0) { mbar_arrive_expect_tx(&bars.k_full[s], PD_HALF); mbar_arrive_expect_tx(&bars.v_full[s], PD_HALF); }
+      __syncwarp();
+      // a page that is not there reads the zero fill (a row past the end)
+      if (lane < ppt) {
+        const int row = y >= 0 ? y : max(1, (int)(((long long)sh.n_pages * sh.Hkv) << sh.page_log2));
+        uint8_t* dst = kv_s + s * 2 * PD_HALF + (lane << sh.page_log2) * 128;
+        tma_load_2d(dst, &tm_k, 0, row, &bars.k_full[s]);
+        tma_load_2d(dst + PD_HALF, &tm_v, 0, row, &bars.v_full[s]);
+      }
+      ++it;
+      if (new_seg && !put_q(seg_now, b_now, u_now)) break;
+      y = y2; ks = ks2; ev = ev2;
     }
     // loads in flight after an abort land before the CTA leaves
     if (lane == 0)
@@ -275,7 +359,6 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
       constexpr uint32_t ID_O = idesc_e4m3(128, N) | (1u << 15);   // A = V^T, MN-major
       int it = 0, seg = 0;
       bool ok = true;
-      const uint32_t q0 = smem_u32(q_s);
       auto issue_pv = [&](int j) -> bool {
         const int s = j % PD_STAGES, pb = j & 1;
         if (!mbar_wait(&bars.p_full[pb], (uint32_t)((j >> 1) & 1), abortp, errp, PD_ERR_P_FULL)) return false;
@@ -291,7 +374,9 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
         return true;
       };
       while (ok && walk.next(sh, seq_len)) {
-        if (!mbar_wait(&bars.q_full, (uint32_t)(seg & 1), abortp, errp, PD_ERR_Q_FULL)) break;
+        const int qb = seg % QB;
+        if (!mbar_wait(&bars.q_full[qb], (uint32_t)((seg / QB) & 1), abortp, errp, PD_ERR_Q_FULL)) break;
+        const uint32_t q0 = smem_u32(q_s + qb * N * 128);
         ++seg;
         for (int i = 0; i < walk.len; ++i, ++it) {
           const int s = it % PD_STAGES;
@@ -303,6 +388,7 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
             mma_e4m3(tmem + (it & 1) * N, smem_desc_sw128(k0 + k * 32, 16, 1024), smem_desc_sw128(q0 + k * 32, 16, 1024),
                      ID_S, k > 0 ? 1u : 0u);
           mma_commit(&bars.s_full[it & 1]);
+          if (i == walk.len - 1) mma_commit(&bars.q_empty[qb]);
           if (i > 0 && !issue_pv(it - 1)) { ok = false; break; }
         }
         if (ok && !issue_pv(it - 1)) ok = false;
@@ -343,53 +429,21 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
         for (int i = 0; i < 16; ++i) x[c + i] = __uint_as_float(r[i]);
       }
     };
-    bool first_seg = true;
+    int seg = 0;
     while (ok && walk.next(sh, seq_len)) {
       const int b = walk.b, hk = walk.u / sh.HG, g0 = (walk.u - hk * sh.HG) * GP;
       const int gc = min(GP, sh.G - g0);
       const size_t row0 = (size_t)b * sh.H + hk * sh.G + g0;
       int lo, t0;
       const int n = pd_range(sh, seq_len, b, lo, t0);
-      // ---- q in two parts; every product with the last segment's q has completed
-      for (int g = warp; g < GP; g += 4) {
-        uint2 v = make_uint2(0u, 0u);
-        if (g < gc) v = reinterpret_cast<const uint2*>(q + (long long)b * sh.q_stride + (long long)(hk * sh.G + g0 + g) * kD)[lane];
-        const float f[4] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
-        float am = 0.f;
-        bool fin = true;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = fabsf(f[i]);
-          fin = fin && a <= 3.402823466e38f;
-          am = fmaxf(am, a <= 3.402823466e38f ? a : 0.f);
-        }
-        am = warp_redux_max(am);
-        fin = __all_sync(0xffffffffu, fin);
-        // am in [2^e, 2^(e+1)): times 2^(7 - e); the exponent is held where both powers are normal
-        const int e = max(-110, (int)(__float_as_uint(am) >> 23) - 127) - 7;
-        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-        uint32_t hi = 0u, lw = 0u;
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          const float a = f[i] * inv, c = f[i + 1] * inv;
-          const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(a, c), __NV_SATFINITE, __NV_E4M3);
-          const float2 d = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2, __NV_E4M3)));
-          const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2((a - d.x) * 16.f, (c - d.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
-          hi |= h2 << (8 * i);
-          lw |= l2 << (8 * i);
-        }
-        *reinterpret_cast<uint32_t*>(q_s + sw128(g, lane >> 2) + (lane & 3) * 4) = hi;
-        *reinterpret_cast<uint32_t*>(q_s + sw128(GP + g, lane >> 2) + (lane & 3) * 4) = lw;
-        // a row of q that is not finite has no finite score
-        if (lane == 0) sm->qs[g] = fin ? sh.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) : __int_as_float(0x7fc00000);
-      }
-      fence_proxy_async_smem();
+      const int qb = seg % QB;
+      wait(&bars.q_full[qb], (uint32_t)((seg / QB) & 1), PD_ERR_Q_FULL);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.q_full);
-      named_bar(1, 128);
       float qs[GP], o[GP], l[GP], R[GP], r_prev[GP], p_prev[GP];
 #pragma unroll
-      for (int g = 0; g < GP; ++g) { qs[g] = sm->qs[g]; o[g] = 0.f; l[g] = 0.f; R[g] = -INFINITY; r_prev[g] = 0.f; p_prev[g] = 0.f; }
+      for (int g = 0; g < GP; ++g) { qs[g] = sm->qs[qb][g]; o[g] = 0.f; l[g] = 0.f; R[g] = -INFINITY; r_prev[g] = 0.f; p_prev[g] = 0.f; }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.q_empty[qb]);
       // tile j's O^T and probabilities join the sums
       auto join = [&](int j) {
         wait(&bars.o_full[j & 1], (uint32_t)((j >> 1) & 1), PD_ERR_O_FULL);
@@ -480,16 +534,16 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
 #pragma unroll
       for (int g = 0; g < GP; ++g) {
         const float t = warp_sum(l[g]);
-        if (lane == 0) sm->lsum[g][warp] = t;
+        if (lane == 0) sm->lsum[seg & 1][g][warp] = t;
       }
       tc_fence_before();
       ok = !named_bar_or(1, 128, !w || *abortp != 0);
       if (!ok) break;
       const bool whole = walk.len == walk.nt;
-      const int slot = 2 * blockIdx.x + (first_seg ? 0 : 1);
+      const int slot = 2 * blockIdx.x + (seg > 0 ? 1 : 0);
 #pragma unroll
       for (int g = 0; g < GP; ++g) {
-        const float lt = (sm->lsum[g][0] + sm->lsum[g][1]) + (sm->lsum[g][2] + sm->lsum[g][3]);
+        const float lt = (sm->lsum[seg & 1][g][0] + sm->lsum[seg & 1][g][1]) + (sm->lsum[seg & 1][g][2] + sm->lsum[seg & 1][g][3]);
         if (whole) {
           if (g < gc) {
             const float inv = lt == 0.f ? 0.f : 1.f / lt;
@@ -501,12 +555,11 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
           if (tid == 0) ws.rl[(size_t)slot * GP + g] = make_float2(R[g], lt);
         }
       }
-      if (first_seg && walk.t > 0 && tid == 0) {
+      if (seg == 0 && walk.t > 0 && tid == 0) {
         int* h = ws.hdr + 8 * blockIdx.x;
         h[0] = b; h[1] = walk.u; h[2] = walk.t; h[3] = walk.nt;
       }
-      first_seg = false;
-      named_bar(1, 128);                                   // lsum and qs are free again
+      ++seg;
     }
   }
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -530,11 +583,11 @@ __global__ void __launch_bounds__(128) page_decode_combine_kernel(PdShape sh, Pd
   if (b < 0) return;
   const long long per = ((long long)h[5] << 32) | (uint32_t)h[4];
   const int u = h[1];
-  const long long a = per * c - h[2], e = a + h[3];        // the unit's tiles
+  const long long a = per * c - h[2], e = a + h[3];        // where the unit's tiles lie in the work
   const int c0 = (int)(a / per), c1 = (int)((e - 1) / per);
   if (c0 != c - 1) return;
   const int hk = u / sh.HG, g0 = (u - hk * sh.HG) * GP, gc = min(GP, sh.G - g0);
-  const int s0 = a == per * c0 ? 2 * c0 : 2 * c0 + 1;
+  const int s0 = a - PD_UNIT <= per * c0 ? 2 * c0 : 2 * c0 + 1;   // the first segment of CTA c0, or its last
   for (int g = blockIdx.y; g < gc; g += gridDim.y) {
     auto slot = [&](int k) { return k == c0 ? s0 : 2 * k; };
     float R = -INFINITY;
@@ -560,7 +613,7 @@ int pd_group(int G) { return G <= 8 ? 8 : 16; }
 
 template <int GP>
 constexpr size_t pd_smem() {
-  return 1024 + (size_t)PD_STAGES * 2 * PD_HALF + 3 * 2 * GP * 128 + sizeof(PdSmall<GP>);
+  return 1024 + (size_t)PD_STAGES * 2 * PD_HALF + (pd_qbufs<GP>() + 2) * 2 * GP * 128 + sizeof(PdSmall<GP>);
 }
 
 template <int GP>
