@@ -13,14 +13,14 @@
 // would be (2^-8). Page scales are powers of two: k's multiplies the score, v's
 // is added to the score's exponent before the exponential, so P V needs no
 // scale of its own, and is taken out again (times 2^-e) for the softmax sum.
-// Each tile has its own reference (its exact maximum, mapped to 2^8): the O^T of
-// a tile is a fresh product, rescaled as it joins the fp32 sum in registers.
+// Each tile has its own reference (its exact maximum, mapped to 2^7 .. 2^8): the O^T
+// of a tile is a fresh product, rescaled as it joins the fp32 sum in registers.
 // So a probability is off by at most 2^-22 of the largest one of its own tile,
 // however flat and long the tail is; a running reference would lose tails of
 // 2^-23 per token.
 //
 // Work. All tiles of all units, in the order of the sequences, are dealt to the
-// CTAs in equal consecutive ranges (two CTAs per SM), whatever the lengths are;
+// CTAs in equal consecutive ranges (two or three CTAs per SM), whatever the lengths are;
 // a unit counts PD_UNIT tiles more for its start and end.
 // A unit that crosses CTAs leaves fp32 partials in the workspace, which
 // page_decode_combine_kernel (a programmatic dependent launch) merges.
@@ -46,32 +46,36 @@ constexpr int PD_THREADS = 192;
 constexpr int PD_PROD_WARP = 4;
 constexpr int PD_MMA_WARP = 5;
 constexpr int PD_TILE = 128;
-constexpr int PD_STAGES = 3;
 constexpr int PD_HALF = PD_TILE * 128;        // 16 KB: K or V codes of a tile
-constexpr int PD_CTAS = 296;                  // two per SM on 148 SMs
+constexpr int PD_SMS = 148;
 constexpr int PD_UNIT = 2;                    // what a unit costs besides its tiles, in tiles
 
 enum { PD_ERR_EMPTY = 1, PD_ERR_K_FULL, PD_ERR_V_FULL, PD_ERR_Q_FULL, PD_ERR_Q_EMPTY, PD_ERR_S_FULL, PD_ERR_P_FULL, PD_ERR_O_FULL,
        PD_ERR_FINAL };
 
+template <int STAGES>
 struct __align__(8) PdBars {
-  uint64_t k_full[PD_STAGES], v_full[PD_STAGES], empty[PD_STAGES];
+  uint64_t k_full[STAGES], v_full[STAGES], empty[STAGES];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t q_full[2], q_empty[2], final_bar;
 };
 
-// Buffers of q's parts: two where two CTAs of an SM have the shared memory for it.
-template <int GP>
-constexpr int pd_qbufs() { return GP == 8 ? 2 : 1; }
+// Depth of the ring and buffers of q's parts, as shared memory allows for GP heads and PER CTAs
+// of an SM. Two CTAs with three stages for pages of 32 tokens and more; three with two for pages
+// of 16, whose many small copies leave a producer behind (8 x up to 131,072 tokens: 311 -> 251 us
+// with pages of 16, but 229 -> 247 us with pages of 128).
+constexpr int pd_stages(int per) { return per == 3 ? 2 : 3; }
+constexpr int pd_qbufs(int gp) { return gp == 8 ? 2 : 1; }
 
-template <int GP>
+template <int GP, int PER>
 struct PdSmall {
-  PdBars bars;
-  float ks[PD_STAGES][8];                     // scale of each page of the tile's keys
-  int ev[PD_STAGES][8];                       // exponent of its values' scale; PD_ABSENT: no such page
+  static constexpr int STAGES = pd_stages(PER);
+  PdBars<STAGES> bars;
+  float ks[STAGES][8];                     // scale of each page of the tile's keys
+  int ev[STAGES][8];                       // exponent of its values' scale; PD_ABSENT: no such page
   __align__(16) float smax[2][GP][4];         // a tile's maxima by warp
-  float lsum[2][GP][4];                       // by segment parity
-  float qs[pd_qbufs<GP>()][GP];                            // what a score of the parts' products is multiplied with
+  __align__(16) float lsum[2][GP][4];         // by segment parity
+  float qs[pd_qbufs(GP)][GP];                            // what a score of the parts' products is multiplied with
   long long scan[PD_THREADS / 32];
   long long x_pre;                            // work before sequence x_b
   int x_b;
@@ -80,6 +84,16 @@ struct PdSmall {
 };
 
 constexpr int PD_ABSENT = 1 << 20;
+
+__device__ __forceinline__ float rcp_approx(float x) {   // within one unit in the last place
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+  return r;
+}
+// 2^d of a whole number d <= 0, 0 below 2^-126 and for NaN.
+__device__ __forceinline__ float pow2i(float d) {
+  return __uint_as_float((__float_as_uint(fmaxf(d, -127.f) + 12582912.f) << 23) + 0x3f800000u);
+}
 
 struct PdShape {
   int B, H, Hkv, G, HG, page_log2, n_pages, max_pages, window;
@@ -145,29 +159,29 @@ struct PdWalk {
 // Partials in the workspace: per CTA a header of 8 ints, then per slot (two per
 // CTA: its first segment, its last one) GP x 128 sums and GP (reference, sum).
 struct PdWs {
-  int* hdr;       // [PD_CTAS][8]: b, u, t, nt, work per CTA (two words); b = -1 when no unit continues here
-  float* o;       // [2 PD_CTAS][GP][128]
-  float2* rl;     // [2 PD_CTAS][GP]
+  int* hdr;       // [CTAs][8]: b, u, t, nt, work per CTA (two words); b = -1 when no unit continues here
+  float* o;       // [2 CTAs][GP][128]
+  float2* rl;     // [2 CTAs][GP]
 };
 
-template <int GP>
-__global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
+template <int GP, int PER>
+__global__ void __launch_bounds__(PD_THREADS, PER) page_decode_sm100_kernel(
     PdShape sh, const uint16_t* __restrict__ q, const float* __restrict__ k_scale, const float* __restrict__ v_scale,
     const int32_t* __restrict__ table, const int32_t* __restrict__ seq_len, uint16_t* __restrict__ out,
     float* __restrict__ lse, PdWs ws, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
-  constexpr int N = 2 * GP, QB = pd_qbufs<GP>();
+  constexpr int N = 2 * GP, QB = pd_qbufs(GP), STAGES = pd_stages(PER);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* kv_s = smem;                                   // [STAGES][K 16 KB | V 16 KB]
-  uint8_t* q_s = kv_s + PD_STAGES * 2 * PD_HALF;          // [QB][N][128 B]
+  uint8_t* q_s = kv_s + STAGES * 2 * PD_HALF;          // [QB][N][128 B]
   uint8_t* p_s = q_s + QB * N * 128;                      // [2][N][128 B]
-  PdSmall<GP>* sm = reinterpret_cast<PdSmall<GP>*>(p_s + 2 * N * 128);
-  PdBars& bars = sm->bars;
+  PdSmall<GP, PER>* sm = reinterpret_cast<PdSmall<GP, PER>*>(p_s + 2 * N * 128);
+  auto& bars = sm->bars;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int HU = sh.Hkv * sh.HG;
 
   if (tid == 0) {
-    for (int s = 0; s < PD_STAGES; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       mbar_init(&bars.k_full[s], 1); mbar_init(&bars.v_full[s], 1); mbar_init(&bars.empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) { mbar_init(&bars.s_full[i], 1); mbar_init(&bars.p_full[i], 4); mbar_init(&bars.o_full[i], 1); }
@@ -317,16 +331,16 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
     bool more = advance();
     if (more) load(walk.b, walk.u, lo, n, t0 + walk.t, y, ks, ev);
     while (more) {
-      const int s = it % PD_STAGES;
+      const int s = it % STAGES;
       const bool new_seg = i == 0;
       const int seg_now = seg, b_now = walk.b, u_now = walk.u;
       int y2 = -1, ev2 = PD_ABSENT;
       float ks2 = 0.f;
       more = advance();
       if (more) load(walk.b, walk.u, lo, n, t0 + walk.t + i, y2, ks2, ev2);
-      if (it >= PD_STAGES) {
+      if (it >= STAGES) {
         bool w = true;
-        if (lane == 0) w = mbar_wait(&bars.empty[s], (uint32_t)((it / PD_STAGES - 1) & 1), abortp, errp, PD_ERR_EMPTY);
+        if (lane == 0) w = mbar_wait(&bars.empty[s], (uint32_t)((it / STAGES - 1) & 1), abortp, errp, PD_ERR_EMPTY);
         if (!__shfl_sync(0xffffffffu, (int)w, 0)) break;
       }
       if (lane < ppt) { sm->ks[s][lane] = ks; sm->ev[s][lane] = ev; }
@@ -346,10 +360,10 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
     }
     // loads in flight after an abort land before the CTA leaves
     if (lane == 0)
-      for (int d = 1; d <= PD_STAGES && it - d >= 0; ++d) {
+      for (int d = 1; d <= STAGES && it - d >= 0; ++d) {
         const int k2 = it - d;
-        mbar_wait_done(&bars.k_full[k2 % PD_STAGES], (uint32_t)((k2 / PD_STAGES) & 1), errp, PD_ERR_K_FULL);
-        mbar_wait_done(&bars.v_full[k2 % PD_STAGES], (uint32_t)((k2 / PD_STAGES) & 1), errp, PD_ERR_V_FULL);
+        mbar_wait_done(&bars.k_full[k2 % STAGES], (uint32_t)((k2 / STAGES) & 1), errp, PD_ERR_K_FULL);
+        mbar_wait_done(&bars.v_full[k2 % STAGES], (uint32_t)((k2 / STAGES) & 1), errp, PD_ERR_V_FULL);
       }
     __syncwarp();
   } else if (warp == PD_MMA_WARP) {
@@ -360,9 +374,9 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
       int it = 0, seg = 0;
       bool ok = true;
       auto issue_pv = [&](int j) -> bool {
-        const int s = j % PD_STAGES, pb = j & 1;
+        const int s = j % STAGES, pb = j & 1;
         if (!mbar_wait(&bars.p_full[pb], (uint32_t)((j >> 1) & 1), abortp, errp, PD_ERR_P_FULL)) return false;
-        if (!mbar_wait(&bars.v_full[s], (uint32_t)((j / PD_STAGES) & 1), abortp, errp, PD_ERR_V_FULL)) return false;
+        if (!mbar_wait(&bars.v_full[s], (uint32_t)((j / STAGES) & 1), abortp, errp, PD_ERR_V_FULL)) return false;
         tc_fence_after();
         const uint32_t v0 = smem_u32(kv_s + s * 2 * PD_HALF + PD_HALF), p0 = smem_u32(p_s + pb * N * 128);
 #pragma unroll
@@ -379,8 +393,8 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
         const uint32_t q0 = smem_u32(q_s + qb * N * 128);
         ++seg;
         for (int i = 0; i < walk.len; ++i, ++it) {
-          const int s = it % PD_STAGES;
-          if (!mbar_wait(&bars.k_full[s], (uint32_t)((it / PD_STAGES) & 1), abortp, errp, PD_ERR_K_FULL)) { ok = false; break; }
+          const int s = it % STAGES;
+          if (!mbar_wait(&bars.k_full[s], (uint32_t)((it / STAGES) & 1), abortp, errp, PD_ERR_K_FULL)) { ok = false; break; }
           tc_fence_after();
           const uint32_t k0 = smem_u32(kv_s + s * 2 * PD_HALF);
 #pragma unroll
@@ -416,9 +430,8 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
       h[5] = (int)(per >> 32);
     }
     auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
-      bool y = true;
-      if (lane == 0) y = mbar_wait(bar, parity, abortp, errp, code);
-      if (!__shfl_sync(0xffffffffu, (int)y, 0)) w = false;
+      if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, abortp, errp, code))) w = false;
     };
     auto load_cols = [&](uint32_t col, float (&x)[N]) {
 #pragma unroll
@@ -438,67 +451,65 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
       const int n = pd_range(sh, seq_len, b, lo, t0);
       const int qb = seg % QB;
       wait(&bars.q_full[qb], (uint32_t)((seg / QB) & 1), PD_ERR_Q_FULL);
-      __syncwarp();
-      float qs[GP], o[GP], l[GP], R[GP], r_prev[GP], p_prev[GP];
+      // The sums o and l are kept relative to 2^R, R the largest reference so far. References are
+      // whole numbers, so that the factors between them are exponents. f: the last tile's factor.
+      float qs[GP], o[GP], l[GP], R[GP], f[GP];
 #pragma unroll
-      for (int g = 0; g < GP; ++g) { qs[g] = sm->qs[qb][g]; o[g] = 0.f; l[g] = 0.f; R[g] = -INFINITY; r_prev[g] = 0.f; p_prev[g] = 0.f; }
+      for (int g = 0; g < GP; ++g) { qs[g] = sm->qs[qb][g]; o[g] = 0.f; l[g] = 0.f; R[g] = -INFINITY; f[g] = 0.f; }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.q_empty[qb]);
-      // tile j's O^T and probabilities join the sums
-      auto join = [&](int j) {
+      auto join = [&](int j) {                            // tile j's O^T joins the sums
         wait(&bars.o_full[j & 1], (uint32_t)((j >> 1) & 1), PD_ERR_O_FULL);
         tc_fence_after();
         float x[N];
         load_cols(2 * N + (j & 1) * N, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int g = 0; g < GP; ++g) {
-          // a tile without a score (reference -inf) adds zeros, one of NaN scores its NaN
-          const float Rn = fmaxf(R[g], r_prev[g]);
-          const float a = R[g] == Rn ? 1.f : ex2_approx(R[g] - Rn);
-          const float f = r_prev[g] > -INFINITY && r_prev[g] != Rn ? ex2_approx(r_prev[g] - Rn) : 1.f;
-          o[g] = fmaf(f, fmaf(x[GP + g], 0.0625f, x[g]), o[g] * a);
-          l[g] = fmaf(f, p_prev[g], l[g] * a);
-          R[g] = Rn;
-        }
+        for (int g = 0; g < GP; ++g) o[g] = fmaf(f[g], fmaf(x[GP + g], 0.0625f, x[g]), o[g]);
       };
       for (int i = 0; i < walk.len; ++i, ++it) {
-        const int s = it % PD_STAGES, sb = it & 1;
+        const int s = it % STAGES, sb = it & 1;
         const int tok = (t0 + walk.t + i) * PD_TILE + tid;
-        wait(&bars.k_full[s], (uint32_t)((it / PD_STAGES) & 1), PD_ERR_K_FULL);   // the page's scales are there
+        wait(&bars.k_full[s], (uint32_t)((it / STAGES) & 1), PD_ERR_K_FULL);   // the page's scales are there
         wait(&bars.s_full[sb], (uint32_t)((it >> 1) & 1), PD_ERR_S_FULL);
-        __syncwarp();
         tc_fence_after();
-        float x[N], p[GP];
-        load_cols(sb * N, x);
+        float p[GP];
         const float ks = sm->ks[s][pg];
         const int ev = sm->ev[s][pg];
         const bool seen = tok >= lo && tok < n && ev != PD_ABSENT;
-        const float evf = (float)ev;
-        tmem_wait_ld();
+        {
+          float x[N];
+          load_cols(sb * N, x);
+          const float evf = (float)ev;
+          tmem_wait_ld();
 #pragma unroll
-        for (int g = 0; g < GP; ++g) {
-          const float sc = fmaf(x[GP + g], 0.0625f, x[g]) * ks;
-          p[g] = seen ? fmaf(sc, qs[g], evf) : -INFINITY;
-          const float mx = warp_redux_max(p[g]);
-          if (lane == 0) sm->smax[sb][g][warp] = mx;
+          for (int g = 0; g < GP; ++g) {
+            const float sc = fmaf(x[GP + g], 0.0625f, x[g]) * ks;
+            p[g] = seen ? fmaf(sc, qs[g], evf) : -INFINITY;
+            const float mx = warp_redux_max(p[g]);
+            if (lane == 0) sm->smax[sb][g][warp] = mx;
+          }
         }
+        if (i > 0) join(it - 1);                          // while the other warps' maxima arrive
         // all scores are read: one vote on the waits, which also publishes the maxima
         ok = !named_bar_or(1, 128, !w || *abortp != 0);
         if (!ok) break;
         const float einv = seen ? __uint_as_float((uint32_t)(127 - ev) << 23) : 0.f;
         uint8_t* pt = p_s + sb * N * 128;
-        float r_now[GP];
 #pragma unroll
         for (int g = 0; g < GP; g += 2) {
           float pr[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float4 m4 = *reinterpret_cast<const float4*>(sm->smax[sb][g + k]);
-            const float mx = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-            r_now[g + k] = mx - 8.f;                       // the tile's largest probability becomes 2^8
-            pr[k] = ex2_approx(p[g + k] - (mx == -INFINITY ? 0.f : r_now[g + k]));
-            p[g + k] = pr[k] * einv;
+            // the tile's largest probability becomes 2^7 .. 2^8; no score at all leaves -inf
+            const float r = ceilf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w))) - 8.f;
+            const float Rn = fmaxf(R[g + k], r), a = pow2i(R[g + k] - Rn);
+            R[g + k] = Rn;
+            f[g + k] = pow2i(r - Rn);
+            pr[k] = ex2_approx(p[g + k] - (r == -INFINITY ? 0.f : r));
+            o[g + k] *= a;
+            l[g + k] = fmaf(f[g + k], pr[k] * einv, l[g + k] * a);
           }
           const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(pr[0], pr[1]), __NV_SATFINITE, __NV_E4M3);
           const float2 d = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2, __NV_E4M3)));
@@ -512,8 +523,7 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
         // a tile with tokens that are not seen: their stale V rows may hold NaN
         const int first = (t0 + walk.t + i) * PD_TILE;
         if (first < lo || first + PD_TILE > n) {
-          wait(&bars.v_full[s], (uint32_t)((it / PD_STAGES) & 1), PD_ERR_V_FULL);
-          __syncwarp();
+          wait(&bars.v_full[s], (uint32_t)((it / STAGES) & 1), PD_ERR_V_FULL);
           if (w && !seen) {
             uint4* row = reinterpret_cast<uint4*>(kv_s + s * 2 * PD_HALF + PD_HALF + tid * 128);
 #pragma unroll
@@ -524,36 +534,46 @@ __global__ void __launch_bounds__(PD_THREADS, 2) page_decode_sm100_kernel(
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_full[sb]);
-        if (i > 0) join(it - 1);
-#pragma unroll
-        for (int g = 0; g < GP; ++g) { r_prev[g] = r_now[g]; p_prev[g] = p[g]; }
       }
       if (!ok) break;
       join(it - 1);
-      // ---- the segment's sums
+      // ---- the segment's sums: l over the warp, halving the heads that a lane holds
 #pragma unroll
-      for (int g = 0; g < GP; ++g) {
-        const float t = warp_sum(l[g]);
-        if (lane == 0) sm->lsum[seg & 1][g][warp] = t;
+      for (int h = GP / 2, m = 16; m > 0; m >>= 1) {
+        if (h > 0) {
+          const bool up = lane & m;
+#pragma unroll
+          for (int g = 0; g < h; ++g) {
+            const float give = up ? l[g] : l[g + h], keep = up ? l[g + h] : l[g];
+            l[g] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+          }
+          h >>= 1;
+        } else {
+          l[0] += __shfl_xor_sync(0xffffffffu, l[0], m);
+        }
       }
+      constexpr int LB = GP == 8 ? 2 : 1;                 // lanes (1 << LB) that hold the same head
+      if ((lane & ((1 << LB) - 1)) == 0) sm->lsum[seg & 1][lane >> LB][warp] = l[0];
       tc_fence_before();
       ok = !named_bar_or(1, 128, !w || *abortp != 0);
       if (!ok) break;
       const bool whole = walk.len == walk.nt;
       const int slot = 2 * blockIdx.x + (seg > 0 ? 1 : 0);
+      float Rt = R[0], lt = 0.f;                          // of head tid
 #pragma unroll
       for (int g = 0; g < GP; ++g) {
-        const float lt = (sm->lsum[seg & 1][g][0] + sm->lsum[seg & 1][g][1]) + (sm->lsum[seg & 1][g][2] + sm->lsum[seg & 1][g][3]);
-        if (whole) {
-          if (g < gc) {
-            const float inv = lt == 0.f ? 0.f : 1.f / lt;
-            out[(row0 + g) * kD + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(o[g] * inv));
-            if (lse != nullptr && tid == 0) lse[row0 + g] = lt == 0.f ? -INFINITY : (R[g] + log2f(lt)) * kLn2;
-          }
-        } else {
+        const float4 l4 = *reinterpret_cast<const float4*>(sm->lsum[seg & 1][g]);
+        const float lg = (l4.x + l4.y) + (l4.z + l4.w);
+        if (tid == g) { Rt = R[g]; lt = lg; }
+        if (!whole)
           ws.o[((size_t)slot * GP + g) * kD + tid] = o[g];
-          if (tid == 0) ws.rl[(size_t)slot * GP + g] = make_float2(R[g], lt);
-        }
+        else if (g < gc)
+          out[(row0 + g) * kD + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(o[g] * (lg == 0.f ? 0.f : rcp_approx(lg))));
+      }
+      if (!whole) {
+        if (tid < GP) ws.rl[(size_t)slot * GP + tid] = make_float2(Rt, lt);
+      } else if (lse != nullptr && tid < gc) {
+        lse[row0 + tid] = lt == 0.f ? -INFINITY : (Rt + log2f(lt)) * kLn2;
       }
       if (seg == 0 && walk.t > 0 && tid == 0) {
         int* h = ws.hdr + 8 * blockIdx.x;
@@ -611,17 +631,17 @@ namespace {
 // groups take 16 heads at a time (N = 32) and read the cache once for each 16.
 int pd_group(int G) { return G <= 8 ? 8 : 16; }
 
-template <int GP>
+template <int GP, int PER>
 constexpr size_t pd_smem() {
-  return 1024 + (size_t)PD_STAGES * 2 * PD_HALF + (pd_qbufs<GP>() + 2) * 2 * GP * 128 + sizeof(PdSmall<GP>);
+  return 1024 + (size_t)pd_stages(PER) * 2 * PD_HALF + (pd_qbufs(GP) + 2) * 2 * GP * 128 + sizeof(PdSmall<GP, PER>);
 }
 
-template <int GP>
+template <int GP, int PER>
 cslc_status pd_launch(const PdShape& sh, const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_cache,
                       const float* k_scale, const float* v_scale, const int32_t* table, const int32_t* seq_len,
                       uint16_t* out, float* lse, uint8_t* wsp, cudaStream_t stream) {
-  cudaError_t err = cudaFuncSetAttribute(page_decode_sm100_kernel<GP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)pd_smem<GP>());
+  cudaError_t err = cudaFuncSetAttribute(page_decode_sm100_kernel<GP, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)pd_smem<GP, PER>());
   if (err != cudaSuccess) return set_error(CSLC_ERR_CUDA, "cslc_page_decode_attn: %s", cudaGetErrorString(err));
   // an empty cache has no page to load; its map only has to be valid
   const uint64_t rows = (uint64_t)sh.n_pages * sh.Hkv << sh.page_log2;
@@ -633,12 +653,13 @@ cslc_status pd_launch(const PdShape& sh, const uint16_t* q, const uint8_t* k_cac
     return set_error(CSLC_ERR_CUDA, "cslc_page_decode_attn: tensor map encoding failed");
   PdWs ws;
   ws.hdr = reinterpret_cast<int*>(wsp);
-  ws.rl = reinterpret_cast<float2*>(wsp + PD_CTAS * 32);
-  ws.o = reinterpret_cast<float*>(wsp + PD_CTAS * 32 + (size_t)2 * PD_CTAS * GP * sizeof(float2));
+  constexpr int most_ctas = PD_SMS * PER;
+  ws.rl = reinterpret_cast<float2*>(wsp + most_ctas * 32);
+  ws.o = reinterpret_cast<float*>(wsp + most_ctas * 32 + (size_t)2 * most_ctas * GP * sizeof(float2));
   const long long most = (long long)sh.B * sh.Hkv * sh.HG *
-                         ((((long long)sh.max_pages << sh.page_log2) + PD_TILE - 1) / PD_TILE);
-  const int grid = (int)(most < 1 ? 1 : most < PD_CTAS ? most : PD_CTAS);
-  page_decode_sm100_kernel<GP><<<grid, PD_THREADS, pd_smem<GP>(), stream>>>(sh, q, k_scale, v_scale, table, seq_len, out,
+                         ((((long long)sh.max_pages << sh.page_log2) + PD_TILE - 1) / PD_TILE + PD_UNIT);
+  const int grid = (int)(most < 1 ? 1 : most < most_ctas ? most : most_ctas);
+  page_decode_sm100_kernel<GP, PER><<<grid, PD_THREADS, pd_smem<GP, PER>(), stream>>>(sh, q, k_scale, v_scale, table, seq_len, out,
                                                                            lse, ws, tm_k, tm_v);
   cslc_status st = check_launch("page_decode_sm100_kernel");
   if (st != CSLC_OK || grid == 1) return st;
@@ -660,7 +681,8 @@ cslc_status pd_launch(const PdShape& sh, const uint16_t* q, const uint8_t* k_cac
 
 size_t page_decode_workspace_bytes(int, int H, int Hkv) {
   const int GP = pd_group(H / Hkv);
-  return PD_CTAS * 32 + (size_t)2 * PD_CTAS * GP * (sizeof(float2) + kD * sizeof(float));
+  const size_t ctas = PD_SMS * (GP == 8 ? 3 : 2);
+  return ctas * 32 + 2 * ctas * GP * (sizeof(float2) + kD * sizeof(float));
 }
 
 cslc_status launch_page_decode(const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
@@ -670,8 +692,8 @@ cslc_status launch_page_decode(const uint16_t* q, const uint8_t* k_cache, const 
   const int G = H / Hkv, GP = pd_group(G);
   const PdShape sh{B, H, Hkv, G, (G + GP - 1) / GP, 31 - __builtin_clz(page), n_pages, max_pages, window, scale * kLog2e, q_stride};
   uint8_t* w = static_cast<uint8_t*>(ws);
-  return GP == 8 ? pd_launch<8>(sh, q, k_cache, v_cache, k_scale, v_scale, table, seq_len, out, lse, w, stream)
-                 : pd_launch<16>(sh, q, k_cache, v_cache, k_scale, v_scale, table, seq_len, out, lse, w, stream);
+  const auto run = GP == 16 ? pd_launch<16, 2> : page == 16 ? pd_launch<8, 3> : pd_launch<8, 2>;
+  return run(sh, q, k_cache, v_cache, k_scale, v_scale, table, seq_len, out, lse, w, stream);
 }
 
 int page_decode_sm100_read_error() {
