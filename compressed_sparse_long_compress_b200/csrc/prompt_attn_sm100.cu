@@ -15,8 +15,8 @@
 //                   so the steady state needs no maximum. P goes back to TMEM
 //                   as bf16 and is the A operand of P V from there: no shared
 //                   memory and no proxy fence.
-//   warp 8          producer: Q tiles, K and V tiles of 64 keys (TMA, 10-deep
-//                   ring of 16 KB)
+//   warp 8          producer: Q tiles (two items), K and V tiles of 64 keys
+//                   (TMA, 6-deep ring of 16 KB)
 //   warps 9, 10     MMA issue for Q tile 0 and 1 (9 also allocates TMEM): S of
 //                   the next tile as soon as this tile's scores are in
 //                   registers, P V of this tile when P is there. So a softmax
@@ -50,7 +50,7 @@ constexpr int PA_PROD_WARP = 8;
 constexpr int PA_MMA_WARP = 9;
 constexpr int PA_ROWS = 128;                     // rows of a Q tile
 constexpr int PA_KEYS = 64;                      // keys of a K or V tile
-constexpr int PA_SLOTS = 10;
+constexpr int PA_SLOTS = 6;
 constexpr int PA_Q_BYTES = PA_ROWS * 256;        // two halves of 64 dims
 constexpr int PA_KV_BYTES = PA_KEYS * 256;
 constexpr int PA_KV_HALF = PA_KEYS * 128;
@@ -59,24 +59,15 @@ constexpr int PA_BUCKETS = 512;
 constexpr int PA_SCHED_THREADS = 1024;
 
 enum { PA_ERR_ITEM = 1, PA_ERR_Q_EMPTY, PA_ERR_EMPTY, PA_ERR_Q_FULL, PA_ERR_K_FULL, PA_ERR_V_FULL, PA_ERR_P_FULL,
-       PA_ERR_O_FREE, PA_ERR_S_FULL, PA_ERR_S_READ, PA_ERR_PV_DONE, PA_ERR_O_FULL, PA_ERR_SCAN, PA_ERR_FINAL };
+       PA_ERR_O_FREE, PA_ERR_S_FULL, PA_ERR_S_READ, PA_ERR_PV_DONE, PA_ERR_O_FULL, PA_ERR_SLOW, PA_ERR_FINAL };
 
 struct __align__(8) PaBars {
   uint64_t full[PA_SLOTS], empty[PA_SLOTS];
-  uint64_t q_full, q_empty;
-  uint64_t s_full[2], s_read[2], o_full[2], o_free[2], scan[2];   // by Q tile
+  uint64_t q_full[2], q_empty[2];                // by item parity
+  uint64_t s_full[2], s_read[2], o_full[2], o_free[2], slow_done[2];   // by Q tile
   uint64_t p_full[2][2], pv_done[2][2];          // [Q tile][buffer]
   uint64_t item_full[2], item_empty[2];
   uint64_t final_bar[2];
-};
-
-struct PaSmall {
-  PaBars bars;
-  int4 item[2];                                  // b, pair, key head; b = -1: no more
-  int bad_v[2][2];                               // [Q tile][parity]: the last scan whose V tile was not finite
-  int skip[2][2];                                // [Q tile][buffer]: this P V is not the tensor cores'
-  uint32_t tmem_base;
-  int abort_flag;
 };
 
 struct PaShape {
@@ -85,11 +76,24 @@ struct PaShape {
   int direct;                                    // no schedule: CTA = item
 };
 
-// One item: two Q tiles of sequence b at its tokens t0 .. t0 + 2 tpt - 1.
+// One item: two Q tiles of a sequence at its tokens t0 .. t0 + 2 tpt - 1.
 struct PaItem {
-  int q0, nq, k0, off, t0;                       // rows of q and k, nk - nq, first token
+  int q0, nq, k0, off, t0;                       // rows of q and k, nk - nq, first token of tile 0
   int n[2], s[2], e[2];                          // per Q tile: tokens, key tiles [s, e)
   int jb, je;
+};
+
+struct PaTake {
+  int there, hk;                                 // an item, its key head; not there: no more
+  PaItem it;
+};
+
+struct PaSmall {
+  PaBars bars;
+  PaTake take[2];                                // by item parity
+  int bad_v[2][2];                               // [Q tile][buffer]: the last tile (from 1) whose V was not finite
+  uint32_t tmem_base;
+  int abort_flag;
 };
 
 __device__ __forceinline__ void pa_seq(const PaShape& sh, const int32_t* __restrict__ cu_q,
@@ -264,8 +268,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
     const __grid_constant__ CUtensorMap tm_v) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* q_s = smem;                                   // [2 tiles][2 halves][128][128 B]
-  uint8_t* ring = q_s + 2 * PA_Q_BYTES;                  // [SLOTS][2 halves][64][128 B]
+  uint8_t* q_s = smem;                                   // [2 items][2 tiles][2 halves][128][128 B]
+  uint8_t* ring = q_s + 4 * PA_Q_BYTES;                  // [SLOTS][2 halves][64][128 B]
   PaSmall* sm = reinterpret_cast<PaSmall*>(ring + PA_SLOTS * PA_KV_BYTES);
   PaBars& bars = sm->bars;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -273,13 +277,13 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
 
   if (tid == 0) {
     for (int s = 0; s < PA_SLOTS; ++s) { mbar_init(&bars.full[s], 1); mbar_init(&bars.empty[s], 2); }
-    mbar_init(&bars.q_full, 1); mbar_init(&bars.q_empty, 2);
     for (int w = 0; w < 2; ++w) {
       for (int i = 0; i < 2; ++i) {
         mbar_init(&bars.p_full[w][i], 4); mbar_init(&bars.pv_done[w][i], 1);
       }
       mbar_init(&bars.s_full[w], 1); mbar_init(&bars.s_read[w], 4);
-      mbar_init(&bars.o_full[w], 1); mbar_init(&bars.o_free[w], 4); mbar_init(&bars.scan[w], 4);
+      mbar_init(&bars.o_full[w], 1); mbar_init(&bars.o_free[w], 4); mbar_init(&bars.slow_done[w], 4);
+      mbar_init(&bars.q_full[w], 1); mbar_init(&bars.q_empty[w], 10);
       mbar_init(&bars.item_full[w], 1); mbar_init(&bars.item_empty[w], 10);
       mbar_init(&bars.final_bar[w], 1);
       sm->bad_v[w][0] = sm->bad_v[w][1] = 0;
@@ -290,7 +294,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
   if (warp == PA_MMA_WARP) tmem_alloc(&sm->tmem_base, 512);
   // rows of no (token, head) are never loaded: zeros, so that their scores are finite
   if (rows < PA_ROWS)
-    for (int i = tid; i < 4 * (PA_ROWS - rows) * 8; i += PA_THREADS) {
+    for (int i = tid; i < 8 * (PA_ROWS - rows) * 8; i += PA_THREADS) {
       const int part = i / ((PA_ROWS - rows) * 8), r = i % ((PA_ROWS - rows) * 8);
       reinterpret_cast<uint4*>(q_s + part * (PA_ROWS * 128) + rows * 128)[r] = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -302,15 +306,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
   const uint32_t tmem = sm->tmem_base;
   volatile int* abortp = &sm->abort_flag;
   int* errp = &g_prompt_attn_err;
-
-  // the item in slot n & 1 of the hand-over, read by every role; false: no more, or a wait gave up
-  auto take_item = [&](int n, int4& x) -> bool {
-    bool ok = true;
-    if (lane == 0) ok = mbar_wait(&bars.item_full[n & 1], (uint32_t)((n >> 1) & 1), abortp, errp, PA_ERR_ITEM);
-    if (__shfl_sync(0xffffffffu, (int)ok, 0) == 0) return false;
-    x = sm->item[n & 1];
-    return x.x >= 0;
-  };
 
   if (warp == PA_PROD_WARP) {
     // ------------------------------------------------------------ producer
@@ -333,16 +328,18 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       };
       const int n_pairs = sh.direct ? 0 : ws.head[1];
       const long long n_items = (long long)n_pairs * sh.Hkv;
-      for (;; ++n) {
-        int4 x = make_int4(-1, 0, 0, 0);
+      auto fetch = [&](bool first) -> PaTake {           // the next item
+        PaTake t;
+        int b = -1, pair = 0;
         if (sh.direct) {
-          if (n == 0) {                                  // item = CTA: the pair by a walk over the sequences
-            int pair = blockIdx.x / sh.Hkv;
-            for (int b = 0; b < sh.B; ++b) {
+          if (first) {                                   // item = CTA: the pair by a walk over the sequences
+            pair = blockIdx.x / sh.Hkv;
+            t.hk = blockIdx.x % sh.Hkv;
+            for (int c = 0; c < sh.B; ++c) {
               int q0, nq, k0, nk;
-              pa_seq(sh, cu_q, cu_k, b, q0, nq, k0, nk);
+              pa_seq(sh, cu_q, cu_k, c, q0, nq, k0, nk);
               const int p = pa_pairs(sh, nq);
-              if (pair < p) { x = make_int4(b, pair, blockIdx.x % sh.Hkv, 0); break; }
+              if (pair < p) { b = c; break; }
               pair -= p;
             }
           }
@@ -350,35 +347,49 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
           const long long i = atomicAdd(ws.head, 1);
           if (i < n_items) {
             const int2 bp = ws.list[i % n_pairs];
-            x = make_int4(bp.x, bp.y, (int)(i / n_pairs), 0);
+            b = bp.x;
+            pair = bp.y;
+            t.hk = (int)(i / n_pairs);
           }
         }
+        t.there = b >= 0;
+        if (b >= 0) t.it = pa_item(sh, cu_q, cu_k, b, pair);
+        return t;
+      };
+      PaTake next = fetch(true);
+      for (;; ++n) {
+        const PaTake t = next;
         if (n >= 2 && !mbar_wait(&bars.item_empty[n & 1], (uint32_t)(((n >> 1) - 1) & 1), abortp, errp, PA_ERR_ITEM)) break;
-        sm->item[n & 1] = x;
+        sm->take[n & 1] = t;
         mbar_arrive(&bars.item_full[n & 1]);
-        if (x.x < 0) break;
-        const PaItem it = pa_item(sh, cu_q, cu_k, x.x, x.y);
-        const int hk = x.z;
-        if (it.jb < it.je && !load_tile(&tm_k, hk, it.k0 + it.jb * PA_KEYS)) break;
-        if (n >= 1 && !mbar_wait(&bars.q_empty, (uint32_t)((n - 1) & 1), abortp, errp, PA_ERR_Q_EMPTY)) break;
+        if (!t.there) break;
+        const PaItem& it = t.it;
+        const int hk = t.hk;
+        if (n >= 2 && !mbar_wait(&bars.q_empty[n & 1], (uint32_t)(((n >> 1) - 1) & 1), abortp, errp, PA_ERR_Q_EMPTY)) break;
         q_loads = n + 1;
-        mbar_arrive_expect_tx(&bars.q_full, (uint32_t)(4 * rows * 128));
+        mbar_arrive_expect_tx(&bars.q_full[n & 1], (uint32_t)(4 * rows * 128));
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const int tok = it.q0 + it.t0 + w * sh.tpt;
-          tma_load_3d(q_s + w * PA_Q_BYTES, &tm_q, 0, hk * sh.G, tok, &bars.q_full);
-          tma_load_3d(q_s + w * PA_Q_BYTES + PA_ROWS * 128, &tm_q, 64, hk * sh.G, tok, &bars.q_full);
+          uint8_t* dst = q_s + ((n & 1) * 2 + w) * PA_Q_BYTES;
+          tma_load_3d(dst, &tm_q, 0, hk * sh.G, tok, &bars.q_full[n & 1]);
+          tma_load_3d(dst + PA_ROWS * 128, &tm_q, 64, hk * sh.G, tok, &bars.q_full[n & 1]);
         }
-        // in the order of use: K0 K1 V0 K2 V1 ..
-        if (it.jb + 1 < it.je) ok = load_tile(&tm_k, hk, it.k0 + (it.jb + 1) * PA_KEYS);
+        // in the order of use: K0 K1 V0 K2 V1 .. The next item is looked up behind the first tiles.
+        if (it.jb < it.je) ok = load_tile(&tm_k, hk, it.k0 + it.jb * PA_KEYS);
+        if (ok && it.jb + 1 < it.je) ok = load_tile(&tm_k, hk, it.k0 + (it.jb + 1) * PA_KEYS);
+        bool fetched = false;
         for (int j = it.jb; j < it.je && ok; ++j) {
           ok = load_tile(&tm_v, hk, it.k0 + j * PA_KEYS);
           if (ok && j + 2 < it.je) ok = load_tile(&tm_k, hk, it.k0 + (j + 2) * PA_KEYS);
+          if (j == it.jb + 1) { next = fetch(false); fetched = true; }
         }
         if (!ok) break;
+        if (!fetched) next = fetch(false);
       }
       // loads in flight after an abort land before the CTA leaves
-      if (q_loads > 0) mbar_wait_done(&bars.q_full, (uint32_t)((q_loads - 1) & 1), errp, PA_ERR_Q_FULL);
+      for (int d = 1; d <= 2 && q_loads - d >= 0; ++d)
+        mbar_wait_done(&bars.q_full[(q_loads - d) & 1], (uint32_t)(((q_loads - d) >> 1) & 1), errp, PA_ERR_Q_FULL);
       for (int d = 1; d <= PA_SLOTS && kv - d >= 0; ++d) {
         const int k2 = kv - d;
         mbar_wait_done(&bars.full[k2 % PA_SLOTS], (uint32_t)((k2 / PA_SLOTS) & 1), errp, PA_ERR_K_FULL);
@@ -395,10 +406,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
     auto uni = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
     // low words of the descriptors of the Q tile and ring slot 0; an offset of x bytes adds x / 16
     const uint64_t d_kmaj = smem_desc_sw128(0, 16, 1024), d_mnmaj = smem_desc_sw128(0, PA_KV_HALF, 1024);
-    const uint32_t q0 = uni(smem_u32(q_s + w * PA_Q_BYTES) >> 4), r0 = smem_u32(ring) >> 4;
+    const uint32_t r0 = smem_u32(ring) >> 4;
     const uint32_t t_s = uni(tmem + w * 128), t_o = uni(tmem + 256 + w * 128);
     int slot = 0, ph = 0;                                // the ring, in the order of use
-    int s_it = 0, p_it = 0, o_it = 0;                    // S and P tiles, items with a tile
+    int s_it = 0, p_it = 0, o_it = 0, slow_it = 0;       // S and P tiles, items with a tile, tiles not done here
     bool ok = true;
     // the slot's products are issued (or it is the other Q tile's alone): release it
     auto release = [&]() {
@@ -408,14 +419,15 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
     };
     for (int n = 0; ok; ++n) {
       if (!mbar_wait(&bars.item_full[n & 1], (uint32_t)((n >> 1) & 1), abortp, errp, PA_ERR_ITEM)) break;
-      const int4 x = sm->item[n & 1];
+      const PaTake t = sm->take[n & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.item_empty[n & 1]);
-      if (x.x < 0) break;
-      const PaItem it = pa_item(sh, cu_q, cu_k, x.x, x.y);
+      if (!t.there) break;
+      const PaItem& it = t.it;
+      const uint32_t q0 = uni(smem_u32(q_s + ((n & 1) * 2 + w) * PA_Q_BYTES) >> 4);
       const int js = uni(w == 0 ? it.s[0] : it.s[1]), je = uni(w == 0 ? it.e[0] : it.e[1]);
       const int jb = uni(it.jb), jend = uni(it.je);
-      if (!mbar_wait(&bars.q_full, (uint32_t)(n & 1), abortp, errp, PA_ERR_Q_FULL)) break;
+      if (!mbar_wait(&bars.q_full[n & 1], (uint32_t)((n >> 1) & 1), abortp, errp, PA_ERR_Q_FULL)) break;
       auto issue_s = [&](int j) {
         ok = ok && mbar_wait(&bars.full[slot], (uint32_t)ph, abortp, errp, PA_ERR_K_FULL);
         if (ok && j >= js && j < je && s_it > 0)         // the last scores are in registers
@@ -436,12 +448,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         }
         release();
         if (j == jend - 1) {                             // every S of the item has read Q
-          if (elect_one()) mma_commit(&bars.q_empty);
+          if (elect_one()) mma_commit(&bars.q_empty[n & 1]);
           __syncwarp();
         }
       };
       if (jb == jend) {
-        if (elect_one()) mma_commit(&bars.q_empty);
+        if (elect_one()) mma_commit(&bars.q_empty[n & 1]);
         __syncwarp();
       }
       if (jb < jend) issue_s(jb);
@@ -459,7 +471,13 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
           if (!ok) break;
           ++p_it;
           tc_fence_after();
-          const bool mine = !reinterpret_cast<volatile int*>(sm->skip[w])[b];
+          // a V tile that is not finite where some row does not see it: the softmax warps did the product
+          const bool mine = reinterpret_cast<volatile int*>(sm->bad_v[w])[b] != p_it;
+          if (!mine) {
+            ok = mbar_wait(&bars.slow_done[w], (uint32_t)(slow_it++ & 1), abortp, errp, PA_ERR_SLOW);
+            if (!ok) break;
+            tc_fence_after();
+          }
           if (elect_one()) {
             if (mine) {
 #pragma unroll
@@ -486,37 +504,26 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_off + w * 128, t_o = tmem + lane_off + 256 + w * 128;
     const float c = sh.scale_log2;
-    int kv0 = 0, t_it = 0, scans = 0, o_it = 0;          // ring position, this Q tile's key tiles, scans, items
+    int kv0 = 0, t_it = 0, o_it = 0;                     // ring position, this Q tile's key tiles, items
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity, int code) -> bool {
       if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abortp, errp, code));
     };
-    // is the V tile at ring position vv finite (slow = false)? two threads to a key; all four warps agree
-    auto scan_v = [&](int vv, bool& slow) -> bool {
+    // is the V tile at ring position vv finite? Two threads to a key; a warp finds out about its 16
+    auto scan_v = [&](int vv, bool& bad) -> bool {
       const int vs = vv % PA_SLOTS, key = row >> 1;
       const uint8_t* v_s = ring + vs * PA_KV_BYTES + (row & 1) * PA_KV_HALF + key * 128;
       if (!wait(&bars.full[vs], (uint32_t)((vv / PA_SLOTS) & 1), PA_ERR_V_FULL)) return false;
-      __syncwarp();
-      uint32_t bad = 0u;
+      uint32_t ones = 0u;                                // an exponent of all ones carries into the sign's place
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const uint4 u = *reinterpret_cast<const uint4*>(v_s + ((k ^ (key & 7)) << 4));
         const uint32_t u4[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)                      // an exponent of all ones
-          bad |= (uint32_t)((u4[i] & 0x7f80u) == 0x7f80u) | (uint32_t)((u4[i] & 0x7f800000u) == 0x7f800000u);
+        for (int i = 0; i < 4; ++i) ones |= ((u4[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
       }
-      // the flag holds the number of the scan: a scan of the same parity only begins when all four
-      // warps have read this one's
-      volatile int* flag = &sm->bad_v[w][scans & 1];
-      if (__any_sync(0xffffffffu, bad != 0u) && lane == 0) *flag = scans + 1;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.scan[w]);
-      if (!wait(&bars.scan[w], (uint32_t)(scans & 1), PA_ERR_SCAN)) return false;
-      __syncwarp();
-      slow = *flag == scans + 1;
-      ++scans;
+      bad = __any_sync(0xffffffffu, ones != 0u);
       return true;
     };
     // O += P V on the CUDA cores, entries with P = 0 left out; the products into O are done
@@ -556,15 +563,17 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       }
       tmem_wait_st();
     };
-    int4 x;
+    const int ti = row / sh.G, inv_g = 65535 / sh.G + 1; // this row's token of the Q tile; r / G = r inv_g >> 16
     for (int n = 0; ok; ++n) {
-      if (!take_item(n, x)) break;
+      if (!wait(&bars.item_full[n & 1], (uint32_t)((n >> 1) & 1), PA_ERR_ITEM)) break;
+      const PaTake t = sm->take[n & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.item_empty[n & 1]);
-      const PaItem it = pa_item(sh, cu_q, cu_k, x.x, x.y);
-      const int hk = x.z;
+      if (!t.there) break;
+      const PaItem& it = t.it;
+      const int hk = t.hk;
       const int tw = it.t0 + w * sh.tpt;                 // the Q tile's first token
-      const int ti = row / sh.G, tok = tw + ti;          // this row's token
+      const int tok = tw + ti;                           // this row's token
       const bool row_ok = ti < it.n[w];
       const int last = tok + it.off;                     // its last key (below 0: none) and first
       const int lo = sh.window > 0 ? max(0, last - sh.window + 1) : 0;
@@ -579,12 +588,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         const bool part = j < whole0 || j >= whole1;
         // ring position of its V: behind the K of up to two tiles more
         const int vv = kv0 + (j - it.jb) + min(j - it.jb + 2, it.je - it.jb);
-        bool slow = false;
         if (!wait(&bars.s_full[w], (uint32_t)(t_it & 1), PA_ERR_S_FULL)) { ok = false; break; }
         // (the PV of two tiles before, which read this tile's P buffer, was issued before these
         // scores, so it is done too)
-        // only now: the tile's scores say that the ring is less than a turn before its V
-        if (part && !scan_v(vv, slow)) { ok = false; break; }
         tc_fence_after();
         uint32_t s[2][32];
         auto at = [&](int k) { return __uint_as_float(s[k >> 5][k & 31]); };
@@ -594,10 +600,16 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.s_read[w]);
-        if (part && row_ok) {
-          const int hi = last + 1 - j * PA_KEYS, l0 = lo - j * PA_KEYS;
+        if (part) {
+          const int hi = row_ok ? last + 1 - j * PA_KEYS : PA_KEYS, l0 = row_ok ? lo - j * PA_KEYS : 0;
+          if (j >= whole1) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k) s[k >> 5][k & 31] = k < hi && k >= l0 ? s[k >> 5][k & 31] : 0xff800000u;
+            for (int k = 0; k < 64; ++k) s[k >> 5][k & 31] = k < hi ? s[k >> 5][k & 31] : 0xff800000u;
+          }
+          if (j < whole0) {
+#pragma unroll
+            for (int k = 0; k < 64; ++k) s[k >> 5][k & 31] = k >= l0 ? s[k >> 5][k & 31] : 0xff800000u;
+          }
         }
         auto row_max = [&]() -> float {
           float mx[4];
@@ -628,11 +640,14 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         float sum = ps[0].x + ps[0].y;
         // a stale reference (the probabilities leave the range), or c m does: the warp redoes the tile
         const bool over = !(sum <= PA_SUM_MAX), redo = __any_sync(0xffffffffu, over) || far;
-        if ((redo || slow) && j > it.s[w]) {             // the products into O are done?
-          if (!wait(&bars.pv_done[w][b ^ 1], (uint32_t)(((t_it - 1) >> 1) & 1), PA_ERR_PV_DONE)) { ok = false; break; }
+        auto last_pv_done = [&]() -> bool {
+          if (j == it.s[w]) return true;
+          const bool y = wait(&bars.pv_done[w][b ^ 1], (uint32_t)(((t_it - 1) >> 1) & 1), PA_ERR_PV_DONE);
           tc_fence_after();
-        }
+          return y;
+        };
         if (redo) {
+          if (!last_pv_done()) { ok = false; break; }
           const float mx = over ? fmaxf(row_max(), m) : m;
           const float alpha = mx > m ? ex2_approx((m - mx) * c) : 1.f;
           m = mx;
@@ -661,20 +676,39 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         l += sum;
         tmem_st32(t_p, pk);
         tmem_wait_st();
-        if (slow) slow_pv(t_p, vv, j == it.s[w]);
-        if (lane == 0 && (warp & 3) == 0) sm->skip[w][b] = slow;
+        if (part) {
+          // now, not before: the tile's scores say that the ring is less than a turn before its V
+          bool bad;
+          if (!scan_v(vv, bad)) { ok = false; break; }
+          if (bad && lane == 0) reinterpret_cast<volatile int*>(sm->bad_v[w])[b] = t_it + 1;
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_full[w][b]);
+        if (part) {                                      // what the other warps found
+          if (!wait(&bars.p_full[w][b], (uint32_t)((t_it >> 1) & 1), PA_ERR_P_FULL)) { ok = false; break; }
+          if (reinterpret_cast<volatile int*>(sm->bad_v[w])[b] == t_it + 1) {
+            if (!last_pv_done()) { ok = false; break; }
+            slow_pv(t_p, vv, j == it.s[w]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.slow_done[w]);
+          }
+        }
       }
       if (!ok) break;
       kv0 += 2 * (it.je - it.jb);
       // ---- epilogue
       const bool any = it.e[w] > it.s[w];
-      if (any && !wait(&bars.o_full[w], (uint32_t)(o_it++ & 1), PA_ERR_O_FULL)) break;
+      // (without a key tile: the Q tile has landed)
+      if (!(any ? wait(&bars.o_full[w], (uint32_t)(o_it++ & 1), PA_ERR_O_FULL)
+                : wait(&bars.q_full[n & 1], (uint32_t)((n >> 1) & 1), PA_ERR_Q_FULL)))
+        break;
       tc_fence_after();
+      // The warp's 32 rows go through the item's Q tile, which every S has read, so that the stores
+      // are whole rows (16 bytes of 32 rows in one store took 4,100 to 5,200 cycles an item).
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const size_t orow = (size_t)(it.q0 + tok) * sh.H + hk * sh.G + (row - ti * sh.G);
+      uint8_t* stage = q_s + ((n & 1) * 2 + w) * PA_Q_BYTES;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t r[32];
@@ -685,25 +719,40 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
 #pragma unroll
           for (int i = 0; i < 32; ++i) r[i] = 0u;
         }
-        if (row_ok) {
-          uint4* dst = reinterpret_cast<uint4*>(out + orow * kD + k * 32);
+        if (row < rows) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float f[8];
             // a row that sees nothing has probabilities 0: its sums are 0
 #pragma unroll
             for (int q = 0; q < 8; ++q) f[q] = l == 0.f ? 0.f : __uint_as_float(r[8 * i + q]) * inv;
-            dst[i] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                pack_bf16x2(f[6], f[7]));
+            *reinterpret_cast<uint4*>(stage + (k >> 1) * (PA_ROWS * 128) + sw128(row, (k & 1) * 4 + i)) =
+                make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
           }
         }
       }
-      if (row_ok && lse != nullptr) lse[orow] = l == 0.f ? -INFINITY : fmaf(m, sh.scale, log2f(l) * kLn2);
+      if (row_ok && lse != nullptr)
+        lse[(size_t)(it.q0 + tok) * sh.H + hk * sh.G + (row - ti * sh.G)] = l == 0.f ? -INFINITY : fmaf(m, sh.scale, log2f(l) * kLn2);
       if (any) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.o_free[w]);
       }
+      __syncwarp();
+      const int full = it.n[w] * sh.G;                   // rows of the tile's tokens
+      uint16_t* dst = out + ((size_t)(it.q0 + tw) * sh.H + hk * sh.G) * kD;
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const int r = (row & ~31) + 2 * i + (lane >> 4), c = lane & 15;
+        if (r < full) {
+          const int t = r * inv_g >> 16, h = r - t * sh.G;
+          *reinterpret_cast<uint4*>(dst + ((size_t)t * sh.H + h) * kD + c * 8) =
+              *reinterpret_cast<const uint4*>(stage + (c >> 3) * (PA_ROWS * 128) + sw128(r, c & 7));
+        }
+      }
+      fence_proxy_async_smem();                          // the next Q tile lands where the rows were
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.q_empty[n & 1]);
     }
   }
   tc_fence_before();
@@ -730,7 +779,7 @@ cslc_status launch_prompt_attn(const uint16_t* q, const uint16_t* k, const uint1
                                long long k_stride, long long v_stride, int window, float scale, uint16_t* out,
                                float* lse, void* wsp, cudaStream_t stream) {
   const char* fn = "cslc_prompt_attn";
-  const size_t smem = 1024 + 2 * PA_Q_BYTES + (size_t)PA_SLOTS * PA_KV_BYTES + sizeof(PaSmall);
+  const size_t smem = 1024 + 4 * PA_Q_BYTES + (size_t)PA_SLOTS * PA_KV_BYTES + sizeof(PaSmall);
   int dev = 0, n_sm = 148;
   cudaError_t err = cudaGetDevice(&dev);
   if (err == cudaSuccess) err = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
