@@ -566,13 +566,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
     const int ti = row / sh.G, inv_g = 65535 / sh.G + 1; // this row's token of the Q tile; r / G = r inv_g >> 16
     for (int n = 0; ok; ++n) {
       if (!wait(&bars.item_full[n & 1], (uint32_t)((n >> 1) & 1), PA_ERR_ITEM)) break;
-      const PaTake t = sm->take[n & 1];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.item_empty[n & 1]);
-      if (!t.there) break;
-      const PaItem& it = t.it;
-      const int hk = t.hk;
+      if (!sm->take[n & 1].there) break;
+      const PaItem& it = sm->take[n & 1].it;             // stays there until the tile is done
       const int tw = it.t0 + w * sh.tpt;                 // the Q tile's first token
+      const int j0 = it.s[w], j1 = it.e[w];
       const int tok = tw + ti;                           // this row's token
       const bool row_ok = ti < it.n[w];
       const int last = tok + it.off;                     // its last key (below 0: none) and first
@@ -582,12 +579,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       const int whole1 = (tw + it.off + 1) / PA_KEYS;
       bool far = false;                                  // c m leaves fp32's range for a row of the warp
       float m = -INFINITY, l = 0.f;
-      for (int j = it.s[w]; j < it.e[w]; ++j, ++t_it) {
+      for (int j = j0; j < j1; ++j, ++t_it) {
         const int b = t_it & 1;
         const uint32_t t_p = t_s + 64 + b * 32;
         const bool part = j < whole0 || j >= whole1;
         // ring position of its V: behind the K of up to two tiles more
-        const int vv = kv0 + (j - it.jb) + min(j - it.jb + 2, it.je - it.jb);
+        auto vv = [&]() { return kv0 + (j - it.jb) + min(j - it.jb + 2, it.je - it.jb); };
         if (!wait(&bars.s_full[w], (uint32_t)(t_it & 1), PA_ERR_S_FULL)) { ok = false; break; }
         // (the PV of two tiles before, which read this tile's P buffer, was issued before these
         // scores, so it is done too)
@@ -641,7 +638,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         // a stale reference (the probabilities leave the range), or c m does: the warp redoes the tile
         const bool over = !(sum <= PA_SUM_MAX), redo = __any_sync(0xffffffffu, over) || far;
         auto last_pv_done = [&]() -> bool {
-          if (j == it.s[w]) return true;
+          if (j == j0) return true;
           const bool y = wait(&bars.pv_done[w][b ^ 1], (uint32_t)(((t_it - 1) >> 1) & 1), PA_ERR_PV_DONE);
           tc_fence_after();
           return y;
@@ -653,7 +650,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
           m = mx;
           l *= alpha;
           far = __any_sync(0xffffffffu, fabsf(m * c) > 1e30f && m != -INFINITY);
-          if (j > it.s[w]) {
+          if (j > j0) {
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
               uint32_t r[32];
@@ -679,7 +676,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         if (part) {
           // now, not before: the tile's scores say that the ring is less than a turn before its V
           bool bad;
-          if (!scan_v(vv, bad)) { ok = false; break; }
+          if (!scan_v(vv(), bad)) { ok = false; break; }
           if (bad && lane == 0) reinterpret_cast<volatile int*>(sm->bad_v[w])[b] = t_it + 1;
         }
         tc_fence_before();
@@ -689,7 +686,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
           if (!wait(&bars.p_full[w][b], (uint32_t)((t_it >> 1) & 1), PA_ERR_P_FULL)) { ok = false; break; }
           if (reinterpret_cast<volatile int*>(sm->bad_v[w])[b] == t_it + 1) {
             if (!last_pv_done()) { ok = false; break; }
-            slow_pv(t_p, vv, j == it.s[w]);
+            slow_pv(t_p, vv(), j == j0);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.slow_done[w]);
@@ -699,7 +696,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       if (!ok) break;
       kv0 += 2 * (it.je - it.jb);
       // ---- epilogue
-      const bool any = it.e[w] > it.s[w];
+      const bool any = j1 > j0;
       // (without a key tile: the Q tile has landed)
       if (!(any ? wait(&bars.o_full[w], (uint32_t)(o_it++ & 1), PA_ERR_O_FULL)
                 : wait(&bars.q_full[n & 1], (uint32_t)((n >> 1) & 1), PA_ERR_Q_FULL)))
@@ -709,7 +706,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       // are whole rows (16 bytes of 32 rows in one store took 4,100 to 5,200 cycles an item).
       const float inv = l == 0.f ? 0.f : 1.f / l;
       uint8_t* stage = q_s + ((n & 1) * 2 + w) * PA_Q_BYTES;
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < 4; ++k) {
         uint32_t r[32];
         if (any) {
@@ -732,7 +729,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         }
       }
       if (row_ok && lse != nullptr)
-        lse[(size_t)(it.q0 + tok) * sh.H + hk * sh.G + (row - ti * sh.G)] = l == 0.f ? -INFINITY : fmaf(m, sh.scale, log2f(l) * kLn2);
+        lse[(size_t)(it.q0 + tok) * sh.H + sm->take[n & 1].hk * sh.G + (row - ti * sh.G)] = l == 0.f ? -INFINITY : fmaf(m, sh.scale, log2f(l) * kLn2);
       if (any) {
         tc_fence_before();
         __syncwarp();
@@ -740,8 +737,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       }
       __syncwarp();
       const int full = it.n[w] * sh.G;                   // rows of the tile's tokens
-      uint16_t* dst = out + ((size_t)(it.q0 + tw) * sh.H + hk * sh.G) * kD;
-#pragma unroll 4
+      uint16_t* dst = out + ((size_t)(it.q0 + tw) * sh.H + sm->take[n & 1].hk * sh.G) * kD;
+#pragma unroll 2
       for (int i = 0; i < 16; ++i) {
         const int r = (row & ~31) + 2 * i + (lane >> 4), c = lane & 15;
         if (r < full) {
@@ -752,7 +749,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       }
       fence_proxy_async_smem();                          // the next Q tile lands where the rows were
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.q_empty[n & 1]);
+      if (lane == 0) {
+        mbar_arrive(&bars.item_empty[n & 1]);
+        mbar_arrive(&bars.q_empty[n & 1]);
+      }
     }
   }
   tc_fence_before();
