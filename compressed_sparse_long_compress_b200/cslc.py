@@ -618,11 +618,14 @@ def prompt_attn(q, k, v, cu_q, cu_k, scale: float, window: int = 0, out=None, ls
         lse = _alloc((Tq, H), F32, dev, stream)
     pl = None if lse is None else _at(lse, F32, "lse", dev, (Tq, H))
     if ws is None:
-        nbytes = LIB.cslc_prompt_attn_workspace_bytes(B, Tq, H, Hkv)
-        ws = _alloc((nbytes,), U8, dev, stream)
-    n_ws = ws.numel()
+        n_ws = LIB.cslc_prompt_attn_workspace_bytes(B, Tq, H, Hkv)
+        if n_ws:
+            ws = _alloc((n_ws,), U8, dev, stream)
+    else:
+        n_ws = ws.numel()
+    p_ws = None if ws is None else _at(ws, U8, "ws", dev, (n_ws,))
     _run_on(dev, stream, LIB.cslc_prompt_attn, pq, pk, pv, p_cu_q, p_cu_k, B, Tq, Tk, H, Hkv, D, qs, ks, vs, window, scale,
-            po, pl, _at(ws, U8, "ws", dev, (n_ws,)), n_ws)
+            po, pl, p_ws, n_ws)
     return out, lse
 
 

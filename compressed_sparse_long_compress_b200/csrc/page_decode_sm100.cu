@@ -112,7 +112,7 @@ __device__ __forceinline__ int pd_range(const PdShape& sh, const int32_t* __rest
 __device__ __forceinline__ int pd_tiles(const PdShape& sh, const int32_t* __restrict__ seq_len, int b) {
   int lo, t0;
   const int n = pd_range(sh, seq_len, b, lo, t0);
-  return (n + PD_TILE - 1) / PD_TILE - t0;
+  return n > 0 ? (n - 1) / PD_TILE + 1 - t0 : 0;
 }
 
 // Work of one unit of sequence b: its tiles and PD_UNIT, nothing without a tile.
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(PD_THREADS, PER) page_decode_sm100_kernel(
         }
         // a tile with tokens that are not seen: their stale V rows may hold NaN
         const int first = (t0 + walk.t + i) * PD_TILE;
-        if (first < lo || first + PD_TILE > n) {
+        if (first < lo || first > n - PD_TILE) {
           wait(&bars.v_full[s], (uint32_t)((it / STAGES) & 1), PD_ERR_V_FULL);
           if (w && !seen) {
             uint4* row = reinterpret_cast<uint4*>(kv_s + s * 2 * PD_HALF + PD_HALF + tid * 128);

@@ -95,17 +95,17 @@ __global__ void __launch_bounds__(PP_THREADS) page_plan_kernel(
     }
     return lo;
   };
-  const int step = gridDim.x * PP_THREADS, at = blockIdx.x * PP_THREADS + tid;
+  const long long step = gridDim.x * PP_THREADS, at = blockIdx.x * PP_THREADS + tid;   // the sizes go up to 2^31 - 1
   // new entries of the tables
-  for (int i = at; i < taken; i += step) {
-    const int b = owner(pg, i);
+  for (long long i = at; i < taken; i += step) {
+    const int b = owner(pg, (int)i);
     table[(size_t)b * max_pages + first_page(b) + (i - pg[b])] = given(i);
   }
   // slots; entries below p0 are the caller's and no CTA writes them
-  for (int t = at; t < max_tokens; t += step) {
+  for (long long t = at; t < max_tokens; t += step) {
     int slot = -1;
     if (t < T) {
-      const int b = owner(tok, t);
+      const int b = owner(tok, (int)t);
       const long long x = (long long)max(old_len[b], 0) + (t - tok[b]);
       const long long j = x >> page_log2;
       if (j < max_pages) {
@@ -135,9 +135,9 @@ __global__ void __launch_bounds__(PP_THREADS) page_plan_kernel(
     lost += n - covered;
   }
   // pages of the free list that are no pages
-  for (int i = tid; i < min(taken, n_free); i += PP_THREADS)
+  for (long long i = tid; i < min(taken, n_free); i += PP_THREADS)
     if (given(i) < 0) {
-      const int b = owner(pg, i);
+      const int b = owner(pg, (int)i);
       const long long x0 = ((long long)first_page(b) + (i - pg[b])) << page_log2;
       const long long o = max(old_len[b], 0), end = o + max(new_len[b], 0);
       lost += min(end, x0 + P) - x0;
@@ -159,8 +159,8 @@ cslc_status launch_page_plan(const int32_t* old_len, const int32_t* new_len, int
     const cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return set_error(CSLC_ERR_CUDA, "cslc_page_plan: %s", cudaGetErrorString(e));
   }
-  const int want = (max_tokens + PP_TOKENS - 1) / PP_TOKENS;
-  const int grid = want < 1 ? 1 : want > 148 ? 148 : want;
+  const int want = max_tokens / PP_TOKENS + 1;
+  const int grid = want > 148 ? 148 : want;
   page_plan_kernel<<<grid, PP_THREADS, smem, stream>>>(old_len, new_len, B, free_pages, n_free, 31 - __builtin_clz(page),
                                                        n_pages, max_pages, max_tokens, table, slots, cu, seq_len,
                                                        status);

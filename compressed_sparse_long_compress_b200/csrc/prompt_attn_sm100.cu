@@ -55,6 +55,7 @@ constexpr int PA_Q_BYTES = PA_ROWS * 256;        // two halves of 64 dims
 constexpr int PA_KV_BYTES = PA_KEYS * 256;
 constexpr int PA_KV_HALF = PA_KEYS * 128;
 constexpr float PA_SUM_MAX = 1.8446744e19f;      // 2^64
+constexpr int PA_SMS = 148;
 constexpr int PA_BUCKETS = 512;
 constexpr int PA_SCHED_THREADS = 1024;
 
@@ -768,9 +769,15 @@ namespace {
 // Q-tile pairs of all sequences at most: a pair for every 2 tpt tokens and one more for each sequence.
 long long pa_most_pairs(int B, int Tq, int tpt) { return (long long)Tq / (2 * tpt) + (B < Tq ? B : Tq); }
 
+// At most one item for each SM: no schedule. (The walk over the sequences is short then.)
+bool pa_direct(int B, int Tq, int H, int Hkv) {
+  return B <= PA_SMS && pa_most_pairs(B, Tq, PA_ROWS / (H / Hkv)) * Hkv <= PA_SMS;
+}
+
 }  // namespace
 
 size_t prompt_attn_workspace_bytes(int B, int Tq, int H, int Hkv) {
+  if (pa_direct(B, Tq, H, Hkv)) return 0;
   return 16 + (size_t)pa_most_pairs(B, Tq, PA_ROWS / (H / Hkv)) * sizeof(int2);
 }
 
@@ -780,15 +787,11 @@ cslc_status launch_prompt_attn(const uint16_t* q, const uint16_t* k, const uint1
                                float* lse, void* wsp, cudaStream_t stream) {
   const char* fn = "cslc_prompt_attn";
   const size_t smem = 1024 + 4 * PA_Q_BYTES + (size_t)PA_SLOTS * PA_KV_BYTES + sizeof(PaSmall);
-  int dev = 0, n_sm = 148;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err == cudaSuccess) err = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
-  if (err == cudaSuccess)
-    err = cudaFuncSetAttribute(prompt_attn_sm100_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t err = cudaFuncSetAttribute(prompt_attn_sm100_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return set_error(CSLC_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(err));
   const int G = H / Hkv, tpt = PA_ROWS / G;
   const long long items = pa_most_pairs(B, Tq, tpt) * Hkv;
-  const PaShape sh{B, Tq, Tk, H, Hkv, G, tpt, window, scale, scale * kLog2e, items <= n_sm ? 1 : 0};
+  const PaShape sh{B, Tq, Tk, H, Hkv, G, tpt, window, scale, scale * kLog2e, pa_direct(B, Tq, H, Hkv) ? 1 : 0};
   CUtensorMap tm_q, tm_k, tm_v;
   // without keys no tile of them is loaded: the maps only have to be valid
   const bool keys = Tk > 0;
@@ -806,7 +809,7 @@ cslc_status launch_prompt_attn(const uint16_t* q, const uint16_t* k, const uint1
     if (st != CSLC_OK) return st;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items < n_sm ? items : n_sm));
+  cfg.gridDim = dim3((unsigned)(items < PA_SMS ? items : PA_SMS));
   cfg.blockDim = dim3(PA_THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

@@ -544,3 +544,176 @@ def test_calls_on_other_streams_and_repeated(C):
     for g in got:
         for a, b in zip(g, want):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# ------------------------------------------------- calls that the above do not make
+
+def test_prompt_captured_with_its_schedule(C):
+    """More items than SMs (a schedule in the workspace), captured and replayed with
+    other lengths and rows."""
+    B, H, Hkv, T = 40, 16, 4, 2600
+    q, k, v = randn((T, H, 128), 1), randn((T, Hkv, 128), 2), randn((T, Hkv, 128), 3)
+    cu, out, lse = i32(np.zeros(B + 1)), torch.zeros(T, H, 128, dtype=BF16, device="cuda"), torch.zeros(T, H, device="cuda")
+    ws = torch.empty(C.prompt_attn_workspace_bytes(B, T, H, Hkv), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        C.prompt_attn(q, k, v, cu, cu, SCALE, 70, out=out, lse=lse, ws=ws)
+    r = np.random.RandomState(3)
+    for i in range(3):
+        n = r.multinomial(T - 100 * i, np.ones(B) / B)
+        c = np.concatenate([[0], np.cumsum(n)])
+        cu.copy_(i32(c))
+        for x in (q, k, v):
+            x.copy_(randn(x.shape, 50 + i))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        C.sync_status()
+        rows = set(r.randint(0, c[-1], 60).tolist())
+        check_attention(out, lse, PO.prompt_attention(f64(q), f64(k), f64(v), c, c, SCALE, 70, rows=rows), 200, f"replay {i}")
+        assert (f64(out)[c[-1]:] == 7).all()
+
+
+def test_prompt_two_graphs_and_an_eager_call_at_once(C):
+    """Each with a workspace of its own, on three streams."""
+    T, H, Hkv = 1500, 16, 4
+    cu = i32([0, 700, 1500])
+    x = [[randn((T, n, 128), 10 * g + i) for i, n in enumerate((H, Hkv, Hkv))] for g in range(3)]
+    want = [C.prompt_attn(*y, cu, cu, SCALE, lse=True) for y in x]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for g in range(2):
+        side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(graph, stream=side):
+            outs.append(C.prompt_attn(*x[g], cu, cu, SCALE, lse=True))
+        graphs.append((graph, side))
+    for _ in range(4):
+        for graph, side in graphs:
+            with torch.cuda.stream(side):
+                graph.replay()
+        got = C.prompt_attn(*x[2], cu, cu, SCALE, lse=True)
+        torch.cuda.synchronize()
+        for a, b in zip(outs + [got], want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    C.sync_status()
+
+
+def test_prompt_many_empty_sequences_few_tokens(C):
+    """8192 sequences, 60 of them with tokens; and lengths beyond the tensors, which are cut."""
+    r = np.random.RandomState(5)
+    n = np.zeros(8192, dtype=np.int64)
+    n[r.choice(8192, 60, replace=False)] = 1
+    c = np.concatenate([[0], np.cumsum(n)])
+    q, k, v = randn((60, 4, 128), 1), randn((60, 2, 128), 2), randn((60, 2, 128), 3)
+    out, lse = C.prompt_attn(q, k, v, i32(c), i32(c), SCALE, lse=True)
+    C.sync_status()
+    check_attention(out, lse, PO.prompt_attention(f64(q), f64(k), f64(v), c, c, SCALE), 1)
+    out, lse = C.prompt_attn(q, k, v, i32([-5, 30, 999]), i32([-7, 30, 2 ** 31 - 1]), SCALE, lse=True)
+    C.sync_status()
+    check_attention(out, lse, PO.prompt_attention(f64(q), f64(k), f64(v), [0, 30, 60], [0, 30, 60], SCALE), 30)
+
+
+def test_prompt_without_keys(C):
+    q, k = randn((70, 4, 128), 1), randn((0, 2, 128), 2)
+    out, lse = C.prompt_attn(q, k, k, i32([0, 30, 70]), i32([0, 0, 0]), SCALE, lse=True)
+    C.sync_status()
+    assert (f64(out) == 0).all() and np.isneginf(f64(lse)).all()
+
+
+def test_prompt_all_values_not_finite(C):
+    q, k, v = randn((300, 4, 128), 1), randn((300, 2, 128), 2), randn((300, 2, 128), 3)
+    v[:] = math.nan
+    out, lse = C.prompt_attn(q, k, v, i32([0, 300]), i32([0, 300]), SCALE, lse=True)
+    C.sync_status()
+    assert np.isnan(f64(out)).all() and np.isfinite(f64(lse)).all()
+    k[::3] = math.nan
+    out, lse = C.prompt_attn(q, k, v, i32([0, 300]), i32([0, 300]), SCALE, lse=True)
+    C.sync_status()
+    assert np.isnan(f64(out)).all() and np.isnan(f64(lse)).all()
+    q[5] = math.inf
+    C.prompt_attn(q, k.zero_(), v.fill_(1), i32([0, 300]), i32([0, 300]), SCALE)
+    C.sync_status()
+
+
+def test_decode_query_not_finite(C):
+    """A head of q that is not finite has no finite output, the others are untouched."""
+    cache = make_cache(30, 2, 64, 4)
+    q = randn((3, 8, 128), 9)
+    table, n = i32(np.random.RandomState(1).randint(0, 30, (3, 9))), i32([500, 64, 1])
+    want, _ = C.page_decode_attn(q, *cache, table, n, SCALE)
+    q2 = q.clone()
+    q2[0, 3, 7], q2[2, 0, 0] = math.inf, math.nan
+    got, lse = C.page_decode_attn(q2, *cache, table, n, SCALE, lse=True)
+    C.sync_status()
+    a, b = f64(got), f64(want)
+    assert np.isnan(a[0, 3]).all() and np.isnan(a[2, 0]).all() and np.isnan(f64(lse)[0, 3])
+    a[0, 3], a[2, 0] = b[0, 3], b[2, 0]
+    assert np.array_equal(a, b)
+
+
+def test_decode_small_and_large_queries(C):
+    """Rows of q from the type's smallest to 1e30 (the parts of q are relative to the row)."""
+    for std in (1e-38, 1e-30, 1e6):
+        run_decode(C, [300, 77], 8, 2, 64, seed=3, q_std=std)
+
+
+def test_decode_empty_cache_and_no_table(C):
+    cache = [x[:0].contiguous() for x in make_cache(1, 2, 16, 1)]
+    q = randn((3, 4, 128), 1)
+    for table in (i32(np.zeros((3, 4))), i32(np.zeros((3, 0)))):
+        out, lse = C.page_decode_attn(q, *cache, table, i32([50, 0, 3]), SCALE, lse=True)
+        C.sync_status()
+        assert (f64(out) == 0).all() and np.isneginf(f64(lse)).all()
+
+
+def test_decode_shared_pages(C):
+    """A common prefix: sequences that hold the same pages."""
+    P = 32
+    cache = make_cache(20, 2, P, 6)
+    r = np.random.RandomState(2)
+    table = np.concatenate([np.tile(r.permutation(8), (5, 1)), 8 + r.randint(0, 12, (5, 4))], axis=1)
+    lens = [300, 256, 257, 384, 100]
+    q = randn((5, 6, 128), 2)
+    out, lse = C.page_decode_attn(q, *cache, i32(table), i32(lens), SCALE, lse=True)
+    C.sync_status()
+    kc, vc, ks, vs = (x.cpu().numpy() for x in cache)
+    ref = PO.page_decode_attention(f64(q), kc, vc, ks.astype(float), vs.astype(float), table, lens, SCALE)
+    check_attention(out, lse, ref, 384)
+
+
+def test_write_rows_far_apart(C):
+    """Keys and values that are views with a row stride of their own, and misaligned ones refused."""
+    kc, ks = empty_cache(6, 2, 16)
+    vc, vs = empty_cache(6, 2, 16)
+    big = randn((50, 9, 128), 4)
+    run_write(C, big[:, 1:3], big[:, 6:8], i32(range(20, 70)), kc, vc, ks, vs)
+    bad = randn((50, 9 * 128 + 4), 4)[:, 4:4 + 256].unflatten(1, (2, 128))
+    with pytest.raises(C.CslcError, match="multiple of 8"):
+        C.page_write_e4m3(bad, bad, i32(range(20, 70)), kc, vc, ks, vs)
+    with pytest.raises(ValueError, match="dense within a row"):
+        C.page_write_e4m3(big[:, 1:5:2], big[:, 1:3], i32(range(20, 70)), kc, vc, ks, vs)
+
+
+def test_binding_refusals_on_the_device(C):
+    q, k = randn((4, 8, 128), 1), randn((4, 2, 128), 2)
+    cu = i32([0, 4])
+    with pytest.raises(ValueError, match="expected"):
+        C.prompt_attn(q, k, k[:3], cu, cu, SCALE)
+    with pytest.raises(C.CslcError, match="scale"):
+        C.prompt_attn(q, k, k, cu, cu, 0.0)
+    with pytest.raises(C.CslcError, match="scale"):
+        C.prompt_attn(q, k, k, cu, cu, math.nan)
+    with pytest.raises(TypeError, match="int32"):
+        C.prompt_attn(q, k, k, cu.long(), cu, SCALE)
+    cache = make_cache(3, 2, 16, 1)
+    with pytest.raises(C.CslcError, match="multiple of H_kv"):
+        C.page_decode_attn(q[:, :7], *cache, i32(np.zeros((4, 2))), i32([1] * 4), SCALE)
+    with pytest.raises(C.CslcError, match="page size"):
+        C.page_decode_attn(q, *[x[:, :, :8].contiguous() if x.dim() == 4 else x for x in cache], i32(np.zeros((4, 2))),
+                           i32([1] * 4), SCALE)
+    with pytest.raises(ValueError, match="max_tokens"):
+        C.page_plan(cu, cu, cu, i32(np.zeros((2, 2))), 16, 4)
