@@ -15,7 +15,7 @@
 // scale of its own, and is taken out again (times 2^-e) for the softmax sum.
 // Each tile has its own reference (its exact maximum, mapped to 2^7 .. 2^8): the O^T
 // of a tile is a fresh product, rescaled as it joins the fp32 sum in registers.
-// So a probability is off by at most 2^-22 of the largest one of its own tile,
+// So a probability is off by at most 2^-21 of the largest one of its own tile,
 // however flat and long the tail is; a running reference would lose tails of
 // 2^-23 per token.
 //
@@ -592,37 +592,46 @@ __global__ void __launch_bounds__(PD_THREADS, PER) page_decode_sm100_kernel(
 }
 
 // CTA c merges the unit that crosses from CTA c - 1 into CTA c, if c is the
-// first border inside it. Thread = dim.
+// first border inside it, for one head. Thread = dim; all partials' references
+// and sums are loaded at once, and their rows eight at a time: the time is that
+// of a few dependent loads, also for a sequence alone that every CTA has a part of.
 template <int GP>
 __global__ void __launch_bounds__(128) page_decode_combine_kernel(PdShape sh, PdWs ws, uint16_t* __restrict__ out,
                                                                   float* __restrict__ lse) {
+  __shared__ float w[PD_SMS * 3];                         // factor of each partial
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int c = blockIdx.x + 1, tid = threadIdx.x;
-  const int* h = ws.hdr + 8 * c;
-  const int b = h[0];
+  const int c = blockIdx.x + 1, g = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  const int4 h = *reinterpret_cast<const int4*>(ws.hdr + 8 * c);   // b, u, t, nt
+  const int2 h2 = *reinterpret_cast<const int2*>(ws.hdr + 8 * c + 4);
+  const int b = h.x;
   if (b < 0) return;
-  const long long per = ((long long)h[5] << 32) | (uint32_t)h[4];
-  const int u = h[1];
-  const long long a = per * c - h[2], e = a + h[3];        // where the unit's tiles lie in the work
-  const int c0 = (int)(a / per), c1 = (int)((e - 1) / per);
+  const long long per = ((long long)h2.y << 32) | (uint32_t)h2.x;
+  const int u = h.y;
+  const long long a = per * c - h.z, e = a + h.w;         // where the unit's tiles lie in the work
+  const int c0 = (int)(a / per), n = (int)((e - 1) / per) - c0 + 1;
   if (c0 != c - 1) return;
-  const int hk = u / sh.HG, g0 = (u - hk * sh.HG) * GP, gc = min(GP, sh.G - g0);
+  const int hk = u / sh.HG, g0 = (u - hk * sh.HG) * GP;
+  if (g >= sh.G - g0) return;
   const int s0 = a - PD_UNIT <= per * c0 ? 2 * c0 : 2 * c0 + 1;   // the first segment of CTA c0, or its last
-  for (int g = blockIdx.y; g < gc; g += gridDim.y) {
-    auto slot = [&](int k) { return k == c0 ? s0 : 2 * k; };
-    float R = -INFINITY;
-    for (int k = c0; k <= c1; ++k) R = fmaxf(R, ws.rl[(size_t)slot(k) * GP + g].x);
-    float l = 0.f, o = 0.f;
-    for (int k = c0; k <= c1; ++k) {
-      const float2 rl = ws.rl[(size_t)slot(k) * GP + g];
-      const float f = rl.x > -INFINITY && rl.x != R ? ex2_approx(rl.x - R) : 1.f;   // -inf: zeros, or NaN scores
-      l = fmaf(rl.y, f, l);
-      o = fmaf(ws.o[((size_t)slot(k) * GP + g) * kD + tid], f, o);
-    }
-    const size_t row = (size_t)b * sh.H + hk * sh.G + g0 + g;
-    out[row * kD + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(o * (l == 0.f ? 0.f : 1.f / l)));
-    if (lse != nullptr && tid == 0) lse[row] = l == 0.f ? -INFINITY : (R + log2f(l)) * kLn2;
+  auto at = [&](int k) { return (size_t)(k == 0 ? s0 : 2 * (c0 + k)) * GP + g; };
+  // every warp finds the largest reference and the sum for itself
+  float R = -INFINITY, l = 0.f;
+  for (int k = lane; k < n; k += 32) R = fmaxf(R, ws.rl[at(k)].x);
+  R = warp_redux_max(R);
+  for (int k = lane; k < n; k += 32) {
+    const float2 rl = ws.rl[at(k)];
+    const float f = rl.x > -INFINITY && rl.x != R ? ex2_approx(rl.x - R) : 1.f;   // -inf: zeros, or NaN scores
+    l = fmaf(rl.y, f, l);
+    w[k] = f;                                             // the same value from each warp
   }
+  l = warp_sum(l);
+  __syncthreads();
+  float o = 0.f;
+#pragma unroll 8
+  for (int k = 0; k < n; ++k) o = fmaf(ws.o[at(k) * kD + tid], w[k], o);
+  const size_t row = (size_t)b * sh.H + hk * sh.G + g0 + g;
+  out[row * kD + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(o * (l == 0.f ? 0.f : 1.f / l)));
+  if (lse != nullptr && tid == 0) lse[row] = l == 0.f ? -INFINITY : (R + log2f(l)) * kLn2;
 }
 
 namespace {

@@ -25,7 +25,7 @@ namespace cslc {
 namespace {
 
 constexpr int PP_THREADS = 512;
-constexpr int PP_TOKENS = 2048;        // slots of one CTA and pass
+constexpr int PP_TOKENS = 512;         // slots of one CTA: one to a thread
 constexpr int PP_MAX_B = 8192;
 
 // Inclusive scan of (a, b) over the block, saturating sums kept in 64 bits.
