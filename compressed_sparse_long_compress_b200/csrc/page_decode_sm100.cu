@@ -32,6 +32,7 @@
 // the sequence's visible range get P = 0 and their V rows are cleared in shared memory,
 // since stale codes may be NaN. All waits are time-bounded.
 
+#include "dependent.cuh"
 #include "sm100.cuh"
 
 namespace cslc {
@@ -192,6 +193,7 @@ __global__ void __launch_bounds__(PD_THREADS, PER) page_decode_sm100_kernel(
   }
   if (warp == PD_MMA_WARP) tmem_alloc(&sm->tmem_base, 4 * N < 32 ? 32 : 4 * N);
 
+  grid_dependency_wait();
   // ---- this CTA's range of the work: a scan over the sequences
   long long x0, x1, per;
   {
@@ -453,9 +455,13 @@ __global__ void __launch_bounds__(PD_THREADS, PER) page_decode_sm100_kernel(
       wait(&bars.q_full[qb], (uint32_t)((seg / QB) & 1), PD_ERR_Q_FULL);
       // The sums o and l are kept relative to 2^R, R the largest reference so far. References are
       // whole numbers, so that the factors between them are exponents. f: the last tile's factor.
-      float qs[GP], o[GP], l[GP], R[GP], f[GP];
+      // Lanes 4 g .. 4 g + 3 hold R of head g (and of head 8 + g), and find the factors for all.
+      constexpr int HL = GP / 8;
+      float qs[GP], o[GP], l[GP], f[GP], R[HL];
 #pragma unroll
-      for (int g = 0; g < GP; ++g) { qs[g] = sm->qs[qb][g]; o[g] = 0.f; l[g] = 0.f; R[g] = -INFINITY; f[g] = 0.f; }
+      for (int g = 0; g < GP; ++g) { qs[g] = sm->qs[qb][g]; o[g] = 0.f; l[g] = 0.f; f[g] = 0.f; }
+#pragma unroll
+      for (int i = 0; i < HL; ++i) R[i] = -INFINITY;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.q_empty[qb]);
       auto join = [&](int j) {                            // tile j's O^T joins the sums
@@ -495,30 +501,47 @@ __global__ void __launch_bounds__(PD_THREADS, PER) page_decode_sm100_kernel(
         ok = !named_bar_or(1, 128, !w || *abortp != 0);
         if (!ok) break;
         const float einv = seen ? __uint_as_float((uint32_t)(127 - ev) << 23) : 0.f;
-        uint8_t* pt = p_s + sb * N * 128;
+        uint8_t* pt = p_s + sb * N * 128 + (tid & 15);
+        float ref[HL], fl[HL], al[HL];
+        bool up = false;
+#pragma unroll
+        for (int k = 0; k < HL; ++k) {
+          float mx = (&sm->smax[sb][8 * k][0])[lane];     // 8 heads x 4 warps
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          // the tile's largest probability becomes 2^7 .. 2^8; no score at all leaves -inf
+          const float r = ceilf(mx) - 8.f, Rn = fmaxf(R[k], r);
+          up = up || r > R[k];
+          fl[k] = pow2i(r - Rn);
+          al[k] = pow2i(R[k] - Rn);
+          ref[k] = r == -INFINITY ? 0.f : r;
+          R[k] = Rn;
+        }
+        if (__any_sync(0xffffffffu, up)) {                // rarely, after the first tiles
+#pragma unroll
+          for (int g = 0; g < GP; ++g) {
+            const float a = __shfl_sync(0xffffffffu, al[g >> 3], 4 * (g & 7));
+            o[g] *= a;
+            l[g] *= a;
+          }
+        }
 #pragma unroll
         for (int g = 0; g < GP; g += 2) {
           float pr[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float4 m4 = *reinterpret_cast<const float4*>(sm->smax[sb][g + k]);
-            // the tile's largest probability becomes 2^7 .. 2^8; no score at all leaves -inf
-            const float r = ceilf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w))) - 8.f;
-            const float Rn = fmaxf(R[g + k], r), a = pow2i(R[g + k] - Rn);
-            R[g + k] = Rn;
-            f[g + k] = pow2i(r - Rn);
-            pr[k] = ex2_approx(p[g + k] - (r == -INFINITY ? 0.f : r));
-            o[g + k] *= a;
-            l[g + k] = fmaf(f[g + k], pr[k] * einv, l[g + k] * a);
+            pr[k] = ex2_approx(p[g + k] - __shfl_sync(0xffffffffu, ref[g >> 3], 4 * ((g + k) & 7)));
+            f[g + k] = __shfl_sync(0xffffffffu, fl[g >> 3], 4 * ((g + k) & 7));
+            l[g + k] = fmaf(f[g + k], pr[k] * einv, l[g + k]);
           }
           const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(pr[0], pr[1]), __NV_SATFINITE, __NV_E4M3);
           const float2 d = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2, __NV_E4M3)));
           const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2((pr[0] - d.x) * 16.f, (pr[1] - d.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
-          const int ck = tid >> 4, by = tid & 15;
-          pt[sw128(g, ck) + by] = (uint8_t)h2;
-          pt[sw128(g + 1, ck) + by] = (uint8_t)(h2 >> 8);
-          pt[sw128(GP + g, ck) + by] = (uint8_t)l2;
-          pt[sw128(GP + g + 1, ck) + by] = (uint8_t)(l2 >> 8);
+          const int ck = tid >> 4;
+          pt[sw128(g, ck)] = (uint8_t)h2;
+          pt[sw128(g + 1, ck)] = (uint8_t)(h2 >> 8);
+          pt[sw128(GP + g, ck)] = (uint8_t)l2;
+          pt[sw128(GP + g + 1, ck)] = (uint8_t)(l2 >> 8);
         }
         // a tile with tokens that are not seen: their stale V rows may hold NaN
         const int first = (t0 + walk.t + i) * PD_TILE;
@@ -559,12 +582,17 @@ __global__ void __launch_bounds__(PD_THREADS, PER) page_decode_sm100_kernel(
       if (!ok) break;
       const bool whole = walk.len == walk.nt;
       const int slot = 2 * blockIdx.x + (seg > 0 ? 1 : 0);
-      float Rt = R[0], lt = 0.f;                          // of head tid
+      // of head tid, which is a head of warp 0
+      float Rt = __shfl_sync(0xffffffffu, R[0], 4 * (lane & 7)), lt = 0.f;
+      if constexpr (HL == 2) {
+        const float R1 = __shfl_sync(0xffffffffu, R[HL - 1], 4 * (lane & 7));
+        if (lane & 8) Rt = R1;
+      }
 #pragma unroll
       for (int g = 0; g < GP; ++g) {
         const float4 l4 = *reinterpret_cast<const float4*>(sm->lsum[seg & 1][g]);
         const float lg = (l4.x + l4.y) + (l4.z + l4.w);
-        if (tid == g) { Rt = R[g]; lt = lg; }
+        if (tid == g) lt = lg;
         if (!whole)
           ws.o[((size_t)slot * GP + g) * kD + tid] = o[g];
         else if (g < gc)
@@ -599,7 +627,7 @@ template <int GP>
 __global__ void __launch_bounds__(128) page_decode_combine_kernel(PdShape sh, PdWs ws, uint16_t* __restrict__ out,
                                                                   float* __restrict__ lse) {
   __shared__ float w[PD_SMS * 3];                         // factor of each partial
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  grid_dependency_wait();
   const int c = blockIdx.x + 1, g = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   const int4 h = *reinterpret_cast<const int4*>(ws.hdr + 8 * c);   // b, u, t, nt
   const int2 h2 = *reinterpret_cast<const int2*>(ws.hdr + 8 * c + 4);
@@ -668,20 +696,12 @@ cslc_status pd_launch(const PdShape& sh, const uint16_t* q, const uint8_t* k_cac
   const long long most = (long long)sh.B * sh.Hkv * sh.HG *
                          ((((long long)sh.max_pages << sh.page_log2) + PD_TILE - 1) / PD_TILE + PD_UNIT);
   const int grid = (int)(most < 1 ? 1 : most < most_ctas ? most : most_ctas);
-  page_decode_sm100_kernel<GP, PER><<<grid, PD_THREADS, pd_smem<GP, PER>(), stream>>>(sh, q, k_scale, v_scale, table, seq_len, out,
-                                                                           lse, ws, tm_k, tm_v);
-  cslc_status st = check_launch("page_decode_sm100_kernel");
-  if (st != CSLC_OK || grid == 1) return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid - 1, sh.G < GP ? sh.G : GP);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, page_decode_combine_kernel<GP>, sh, ws, out, lse);
+  err = launch_after(page_decode_sm100_kernel<GP, PER>, dim3(grid), dim3(PD_THREADS), pd_smem<GP, PER>(), stream, sh, q,
+                         k_scale, v_scale, table, seq_len, out, lse, ws, tm_k, tm_v);
+  if (err != cudaSuccess) return set_error(CSLC_ERR_CUDA, "page_decode_sm100_kernel: %s", cudaGetErrorString(err));
+  if (grid == 1) return CSLC_OK;
+  err = launch_after(page_decode_combine_kernel<GP>, dim3(grid - 1, sh.G < GP ? sh.G : GP), dim3(128), 0, stream, sh, ws,
+                         out, lse);
   if (err != cudaSuccess) return set_error(CSLC_ERR_CUDA, "page_decode_combine_kernel: %s", cudaGetErrorString(err));
   return CSLC_OK;
 }

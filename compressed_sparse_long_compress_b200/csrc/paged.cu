@@ -18,7 +18,7 @@
 // One CTA holds a run in registers between the maximum and the conversion, so
 // the input is read once; HBM bound.
 
-#include "common.cuh"
+#include "dependent.cuh"
 
 namespace cslc {
 
@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(PP_THREADS) page_plan_kernel(
     int32_t* __restrict__ table, int32_t* __restrict__ slots, int32_t* __restrict__ cu,
     int32_t* __restrict__ seq_len, int32_t* __restrict__ status) {
   extern __shared__ int32_t pp_smem[];
+  grid_dependency_wait();
   int32_t* tok = pp_smem;              // [B + 1] tokens before sequence b
   int32_t* pg = tok + B + 1;           // [B + 1] pages handed out before sequence b
   __shared__ long long wsum[PP_THREADS / 32][2];
@@ -161,10 +162,11 @@ cslc_status launch_page_plan(const int32_t* old_len, const int32_t* new_len, int
   }
   const int want = max_tokens / PP_TOKENS + 1;
   const int grid = want > 148 ? 148 : want;
-  page_plan_kernel<<<grid, PP_THREADS, smem, stream>>>(old_len, new_len, B, free_pages, n_free, 31 - __builtin_clz(page),
-                                                       n_pages, max_pages, max_tokens, table, slots, cu, seq_len,
-                                                       status);
-  return check_launch("page_plan_kernel");
+  const cudaError_t e = launch_after(page_plan_kernel, dim3(grid), dim3(PP_THREADS), smem, stream, old_len, new_len, B,
+                                         free_pages, n_free, 31 - __builtin_clz(page), n_pages, max_pages, max_tokens,
+                                         table, slots, cu, seq_len, status);
+  if (e != cudaSuccess) return set_error(CSLC_ERR_CUDA, "page_plan_kernel: %s", cudaGetErrorString(e));
+  return CSLC_OK;
 }
 
 // ---------------------------------------------------------------- cache write
@@ -213,6 +215,7 @@ __global__ void __launch_bounds__(PW_THREADS, 4) page_write_kernel(
     const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, const int32_t* __restrict__ slots, int T, int W,
     int R, int Hkv, int page_log2, int n_pages, long long k_stride, long long v_stride, uint8_t* __restrict__ k_cache,
     uint8_t* __restrict__ v_cache, float* __restrict__ k_scale, float* __restrict__ v_scale) {
+  grid_dependency_wait();
   __shared__ int s_slot[2 * PW_MAX_PAGE + 1];            // slots of tokens w0 - 1 .. w0 + W + P - 1
   __shared__ uint32_t s_break[2 * PW_MAX_PAGE / 32 + 1]; // bit t: token w0 + t does not continue a run
   __shared__ float s_max[PW_THREADS / 32];
@@ -352,9 +355,11 @@ cslc_status launch_page_write(const uint16_t* k, const uint16_t* v, const int32_
   int R = 1;
   while (R < 8 && (2 * Hkv) % (2 * R) == 0 && (long long)((T + W - 1) / W) * (2 * Hkv / (2 * R)) >= 8 * 148) R *= 2;
   const unsigned grid = (unsigned)((T + W - 1) / W) * (unsigned)(2 * Hkv / R);
-  page_write_kernel<<<grid, page < 32 ? 64 : 2 * page, 0, stream>>>(k, v, slots, T, W, R, Hkv, 31 - __builtin_clz(page), n_pages, k_stride,
-                                                     v_stride, k_cache, v_cache, k_scale, v_scale);
-  return check_launch("page_write_kernel");
+  const cudaError_t e = launch_after(page_write_kernel, dim3(grid), dim3(page < 32 ? 64 : 2 * page), 0, stream, k, v,
+                                         slots, T, W, R, Hkv, 31 - __builtin_clz(page), n_pages, k_stride, v_stride,
+                                         k_cache, v_cache, k_scale, v_scale);
+  if (e != cudaSuccess) return set_error(CSLC_ERR_CUDA, "page_write_kernel: %s", cudaGetErrorString(e));
+  return CSLC_OK;
 }
 
 }  // namespace cslc

@@ -35,6 +35,7 @@
 // finite its P V is done on the CUDA cores, without the masked entries.
 // All waits are time-bounded; no barrier without a bound is used in the loop.
 
+#include "dependent.cuh"
 #include "sm100.cuh"
 
 namespace cslc {
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__(PA_SCHED_THREADS) prompt_schedule_kernel(PaSha
   __shared__ int bucket[PA_BUCKETS];
   __shared__ int most_s;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");   // the attention's CTAs set up meanwhile
+  grid_dependency_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int each = (sh.B + PA_SCHED_THREADS - 1) / PA_SCHED_THREADS;
   const int b0 = min(sh.B, tid * each), b1 = min(sh.B, b0 + each);
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the schedule
+  grid_dependency_wait();                                // the schedule, or what precedes the call
   const uint32_t tmem = sm->tmem_base;
   volatile int* abortp = &sm->abort_flag;
   int* errp = &g_prompt_attn_err;
@@ -804,21 +806,12 @@ cslc_status launch_prompt_attn(const uint16_t* q, const uint16_t* k, const uint1
   ws.list = reinterpret_cast<int2*>(static_cast<uint8_t*>(wsp) + 16);
   ws.cap = (int)pa_most_pairs(B, Tq, tpt);
   if (!sh.direct) {
-    prompt_schedule_kernel<<<1, PA_SCHED_THREADS, (size_t)(B + 1) * sizeof(int), stream>>>(sh, cu_q, cu_k, ws);
-    const cslc_status st = check_launch("prompt_schedule_kernel");
-    if (st != CSLC_OK) return st;
+    err = launch_after(prompt_schedule_kernel, dim3(1), dim3(PA_SCHED_THREADS), (size_t)(B + 1) * sizeof(int), stream, sh,
+                           cu_q, cu_k, ws);
+    if (err != cudaSuccess) return set_error(CSLC_ERR_CUDA, "prompt_schedule_kernel: %s", cudaGetErrorString(err));
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items < PA_SMS ? items : PA_SMS));
-  cfg.blockDim = dim3(PA_THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = sh.direct ? 0 : 1;                      // a dependent of the schedule only
-  err = cudaLaunchKernelEx(&cfg, prompt_attn_sm100_kernel, sh, cu_q, cu_k, ws, out, lse, tm_q, tm_k, tm_v);
+  err = launch_after(prompt_attn_sm100_kernel, dim3((unsigned)(items < PA_SMS ? items : PA_SMS)), dim3(PA_THREADS), smem,
+                         stream, sh, cu_q, cu_k, ws, out, lse, tm_q, tm_k, tm_v);
   if (err != cudaSuccess) return set_error(CSLC_ERR_CUDA, "prompt_attn_sm100_kernel: %s", cudaGetErrorString(err));
   return CSLC_OK;
 }
