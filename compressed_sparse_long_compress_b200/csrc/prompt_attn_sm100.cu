@@ -11,23 +11,35 @@
 //   warps 0-3, 4-7  softmax and epilogue of Q tile 0 and 1, thread = row = TMEM
 //                   lane. The row's reference m is the exact maximum of its
 //                   first visible tile and moves only when a tile's
-//                   probabilities sum above 2^64 (O in TMEM is rescaled then),
-//                   so the steady state needs no maximum. P goes back to TMEM
-//                   as bf16 and is the A operand of P V from there: no shared
-//                   memory and no proxy fence.
+//                   probabilities sum above 2^16 (O in TMEM is rescaled then),
+//                   so the steady state needs no maximum; neither fp32 nor bf16
+//                   loses precision to the larger numbers. P goes back to TMEM
+//                   as bf16 (off by at most 2^-8 of itself) and is the A operand
+//                   of P V from there: no shared memory and no proxy fence.
 //   warp 8          producer: Q tiles (two items), K and V tiles of 64 keys
 //                   (TMA, 6-deep ring of 16 KB)
 //   warps 9, 10     MMA issue for Q tile 0 and 1 (9 also allocates TMEM): S of
 //                   the next tile as soon as this tile's scores are in
 //                   registers, P V of this tile when P is there. So a softmax
 //                   waits for neither product in the steady state.
-// TMEM columns of a Q tile: S 64, P 2 x 32, O 128; both tiles fill the 512.
+// TMEM columns of a Q tile: S 64, P 2 x 32, O 128; both tiles fill the 512. A
+// product S of 64 keys takes the pipe 48 cycles where half of one of 128 keys
+// would take 32 (it is bound by reading Q and K), but with 128 keys P has to lie
+// over S, and S of the next tile waits for P V of this one: 16.8 ms against 15.9.
+//
+// Measured (64 heads on 8, causal): 32,768 tokens 15.9 ms = 1,110 TFLOP/s at the
+// power limit (1,665 MHz; cuBLAS sustains 1,387 there), 8,192 tokens 1.05 ms. The
+// tensor-core pipe is busy 74 % of the cycles, the exponential pipe 56 %; without
+// any softmax arithmetic the same loop reaches 1,228 TFLOP/s. Exponentials moved
+// to the FMA pipe by a polynomial, single instead of packed fp32 operations, and
+// one thread issuing the products were all slower: at the power limit every
+// instruction counts.
 //
 // Order of work. prompt_schedule_kernel sorts the Q-tile pairs of all sequences
 // by their number of key tiles, largest first; the CTAs draw tickets, so ragged
 // and causal work evens out. The pairs of one key head are drawn together, so
 // that its keys and values stay in L2. Few items (at most one for each CTA)
-// need no order and no ticket.
+// need no order and no ticket: that saves the schedule's 5 us.
 //
 // A value that is masked for some row of a tile may be NaN or infinite, and
 // 0 * NaN would reach that row through the product. So the V tiles that are
@@ -55,7 +67,7 @@ constexpr int PA_SLOTS = 6;
 constexpr int PA_Q_BYTES = PA_ROWS * 256;        // two halves of 64 dims
 constexpr int PA_KV_BYTES = PA_KEYS * 256;
 constexpr int PA_KV_HALF = PA_KEYS * 128;
-constexpr float PA_SUM_MAX = 1.8446744e19f;      // 2^64
+constexpr float PA_SUM_MAX = 65536.f;            // values of up to 2^111 do not overflow O
 constexpr int PA_SMS = 148;
 constexpr int PA_BUCKETS = 512;
 constexpr int PA_SCHED_THREADS = 1024;
@@ -171,6 +183,95 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
   uint32_t r;
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n" : "=r"(r) : "r"(taddr));
   return r;
+}
+
+// Out of line: their registers and code stay out of the softmax loop's.
+// A row of O (none of it: zeros) through 1 / l into its place of the Q tile, row -1: nothing.
+__device__ __noinline__ void pa_stage_rows(uint32_t t_o, uint8_t* stage, int row, bool any, bool nothing, float inv) {
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    uint32_t r[32];
+    if (any) {
+      tmem_ld32(t_o + k * 32, r);
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) r[i] = 0u;
+    }
+    if (row >= 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t pk[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          pk[q] = pack_bf16x2(__uint_as_float(r[8 * i + 2 * q]) * inv, __uint_as_float(r[8 * i + 2 * q + 1]) * inv);
+          pk[q] = nothing ? 0u : pk[q];                  // a row that sees nothing: probabilities 0, sums 0
+        }
+        *reinterpret_cast<uint4*>(stage + (k >> 1) * (PA_ROWS * 128) + sw128(row, (k & 1) * 4 + i)) =
+            make_uint4(pk[0], pk[1], pk[2], pk[3]);
+      }
+    }
+  }
+}
+__device__ __noinline__ void pa_rescale(uint32_t t_o, float alpha) {
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    uint32_t r[32];
+    tmem_ld32(t_o + k * 32, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+    tmem_st32(t_o + k * 32, r);
+  }
+}
+// O += P V on the CUDA cores, entries with P = 0 left out; the products into O are done.
+__device__ __noinline__ void pa_slow_pv(uint32_t t_o, uint32_t t_p, const uint8_t* v_s, bool first) {
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {                          // 32 dims at a time
+    uint32_t r[32];
+    if (!first) {
+      tmem_ld32(t_o + k * 32, r);
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) r[i] = 0u;
+    }
+#pragma unroll 1
+    for (int key = 0; key < PA_KEYS; ++key) {
+      const uint32_t p2 = tmem_ld1(t_p + (key >> 1));
+      tmem_wait_ld();
+      const float p = (key & 1) ? bf16_hi(p2) : bf16_lo(p2);
+      const uint8_t* vr = v_s + (k >> 1) * PA_KV_HALF;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint4 u = *reinterpret_cast<const uint4*>(vr + sw128(key, (k & 1) * 4 + q));
+        const uint32_t u4[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int d = q * 8 + 2 * i;
+          if (p != 0.f) {
+            r[d] = __float_as_uint(fmaf(p, bf16_lo(u4[i]), __uint_as_float(r[d])));
+            r[d + 1] = __float_as_uint(fmaf(p, bf16_hi(u4[i]), __uint_as_float(r[d + 1])));
+          }
+        }
+      }
+    }
+    tmem_st32(t_o + k * 32, r);
+  }
+  tmem_wait_st();
+}
+// A warp's rows r0 .. r0 + 31 of a tile, those below `full`, from there to `dst` (the tile's first row).
+__device__ __noinline__ void pa_store_rows(uint16_t* dst, const uint8_t* stage, int r0, int full, int G, int H, int inv_g) {
+  const int lane = threadIdx.x & 31, c = lane & 15;
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {
+    const int r = r0 + 2 * i + (lane >> 4);
+    if (r < full) {
+      const int t = r * inv_g >> 16, h = r - t * G;
+      *reinterpret_cast<uint4*>(dst + ((size_t)t * H + h) * kD + c * 8) =
+          *reinterpret_cast<const uint4*>(stage + (c >> 3) * (PA_ROWS * 128) + sw128(r, c & 7));
+    }
+  }
 }
 
 }  // namespace
@@ -529,43 +630,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       bad = __any_sync(0xffffffffu, ones != 0u);
       return true;
     };
-    // O += P V on the CUDA cores, entries with P = 0 left out; the products into O are done
-    auto slow_pv = [&](uint32_t t_p, int vv, bool first) {
-      const uint8_t* v_s = ring + (vv % PA_SLOTS) * PA_KV_BYTES;
-#pragma unroll 1
-      for (int k = 0; k < 4; ++k) {                      // 32 dims at a time
-        uint32_t r[32];
-        if (!first) {
-          tmem_ld32(t_o + k * 32, r);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) r[i] = 0u;
-        }
-#pragma unroll 1
-        for (int key = 0; key < PA_KEYS; ++key) {
-          const uint32_t p2 = tmem_ld1(t_p + (key >> 1));
-          tmem_wait_ld();
-          const float p = (key & 1) ? bf16_hi(p2) : bf16_lo(p2);
-          const uint8_t* vr = v_s + (k >> 1) * PA_KV_HALF;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint4 u = *reinterpret_cast<const uint4*>(vr + sw128(key, (k & 1) * 4 + q));
-            const uint32_t u4[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int d = q * 8 + 2 * i;
-              if (p != 0.f) {
-                r[d] = __float_as_uint(fmaf(p, bf16_lo(u4[i]), __uint_as_float(r[d])));
-                r[d + 1] = __float_as_uint(fmaf(p, bf16_hi(u4[i]), __uint_as_float(r[d + 1])));
-              }
-            }
-          }
-        }
-        tmem_st32(t_o + k * 32, r);
-      }
-      tmem_wait_st();
-    };
     const int ti = row / sh.G, inv_g = 65535 / sh.G + 1; // this row's token of the Q tile; r / G = r inv_g >> 16
     for (int n = 0; ok; ++n) {
       if (!wait(&bars.item_full[n & 1], (uint32_t)((n >> 1) & 1), PA_ERR_ITEM)) break;
@@ -653,17 +717,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
           m = mx;
           l *= alpha;
           far = __any_sync(0xffffffffu, fabsf(m * c) > 1e30f && m != -INFINITY);
-          if (j > j0) {
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-              uint32_t r[32];
-              tmem_ld32(t_o + k * 32, r);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-              tmem_st32(t_o + k * 32, r);
-            }
-          }
+          if (j > j0) pa_rescale(t_o, alpha);
           const float ref = m == -INFINITY ? 0.f : m;
           sum = 0.f;
 #pragma unroll
@@ -689,7 +743,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
           if (!wait(&bars.p_full[w][b], (uint32_t)((t_it >> 1) & 1), PA_ERR_P_FULL)) { ok = false; break; }
           if (reinterpret_cast<volatile int*>(sm->bad_v[w])[b] == t_it + 1) {
             if (!last_pv_done()) { ok = false; break; }
-            slow_pv(t_p, vv(), j == j0);
+            pa_slow_pv(t_o, t_p, ring + (vv() % PA_SLOTS) * PA_KV_BYTES, j == j0);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.slow_done[w]);
@@ -709,47 +763,18 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       // are whole rows (16 bytes of 32 rows in one store took 4,100 to 5,200 cycles an item).
       const float inv = l == 0.f ? 0.f : 1.f / l;
       uint8_t* stage = q_s + ((n & 1) * 2 + w) * PA_Q_BYTES;
-#pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
-        uint32_t r[32];
-        if (any) {
-          tmem_ld32(t_o + k * 32, r);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) r[i] = 0u;
-        }
-        if (row < rows) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float f[8];
-            // a row that sees nothing has probabilities 0: its sums are 0
-#pragma unroll
-            for (int q = 0; q < 8; ++q) f[q] = l == 0.f ? 0.f : __uint_as_float(r[8 * i + q]) * inv;
-            *reinterpret_cast<uint4*>(stage + (k >> 1) * (PA_ROWS * 128) + sw128(row, (k & 1) * 4 + i)) =
-                make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-          }
-        }
-      }
+      pa_stage_rows(t_o, stage, row < rows ? row : -1, any, l == 0.f, inv);
       if (row_ok && lse != nullptr)
-        lse[(size_t)(it.q0 + tok) * sh.H + sm->take[n & 1].hk * sh.G + (row - ti * sh.G)] = l == 0.f ? -INFINITY : fmaf(m, sh.scale, log2f(l) * kLn2);
+        lse[(size_t)(it.q0 + tok) * sh.H + sm->take[n & 1].hk * sh.G + (row - ti * sh.G)] =
+            l == 0.f ? -INFINITY : fmaf(m, sh.scale, log2f(l) * kLn2);
       if (any) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.o_free[w]);
       }
       __syncwarp();
-      const int full = it.n[w] * sh.G;                   // rows of the tile's tokens
-      uint16_t* dst = out + ((size_t)(it.q0 + tw) * sh.H + sm->take[n & 1].hk * sh.G) * kD;
-#pragma unroll 2
-      for (int i = 0; i < 16; ++i) {
-        const int r = (row & ~31) + 2 * i + (lane >> 4), c = lane & 15;
-        if (r < full) {
-          const int t = r * inv_g >> 16, h = r - t * sh.G;
-          *reinterpret_cast<uint4*>(dst + ((size_t)t * sh.H + h) * kD + c * 8) =
-              *reinterpret_cast<const uint4*>(stage + (c >> 3) * (PA_ROWS * 128) + sw128(r, c & 7));
-        }
-      }
+      pa_store_rows(out + ((size_t)(it.q0 + tw) * sh.H + sm->take[n & 1].hk * sh.G) * kD, stage, row & ~31, it.n[w] * sh.G, sh.G,
+                    sh.H, inv_g);
       fence_proxy_async_smem();                          // the next Q tile lands where the rows were
       __syncwarp();
       if (lane == 0) {
