@@ -582,7 +582,7 @@ cslc_status cslc_page_write_e4m3(const cslc_bf16* k, const cslc_bf16* v, const i
 }
 
 size_t cslc_prompt_attn_workspace_bytes(int B, int Tq, int H, int Hkv) {
-  if (B <= 0 || Tq <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0) return 0;
+  if (B <= 0 || Tq <= 0 || H <= 0 || H > 128 || Hkv <= 0 || H % Hkv != 0) return 0;
   return prompt_attn_workspace_bytes(B, Tq, H, Hkv);
 }
 
@@ -613,7 +613,7 @@ cslc_status cslc_prompt_attn(const cslc_bf16* q, const cslc_bf16* k, const cslc_
 }
 
 size_t cslc_page_decode_workspace_bytes(int B, int H, int Hkv) {
-  if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0) return 0;
+  if (B <= 0 || H <= 0 || H > 128 || Hkv <= 0 || H % Hkv != 0) return 0;
   return page_decode_workspace_bytes(B, H, Hkv);
 }
 

@@ -174,6 +174,13 @@ def test_decode_refusals():
         assert _decode(ws=None, nws=0)[0] == 5 and _decode(nws=1)[0] == 5
 
 
+def test_workspace_of_head_counts_that_are_refused():
+    """The binding asks for the size before the call checks its arguments."""
+    for H, Hkv in ((256, 1), (129, 1), (1 << 20, 1), (0, 1), (8, 0), (8, 3), (-8, 1), (8, -1)):
+        assert cslc.prompt_attn_workspace_bytes(1, 10, H, Hkv) == 0, (H, Hkv)
+        assert cslc.page_decode_workspace_bytes(1, H, Hkv) == 0, (H, Hkv)
+
+
 def test_binding_refuses_what_it_cannot_pass_on():
     q = torch.zeros(4, 8, 128, dtype=torch.bfloat16)
     cu = torch.zeros(2, dtype=torch.int32)
