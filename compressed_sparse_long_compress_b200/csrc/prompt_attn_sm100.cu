@@ -813,6 +813,7 @@ cslc_status launch_prompt_attn(const uint16_t* q, const uint16_t* k, const uint1
                                long long k_stride, long long v_stride, int window, float scale, uint16_t* out,
                                float* lse, void* wsp, cudaStream_t stream) {
   const char* fn = "cslc_prompt_attn";
+  if (window >= Tk) window = 0;                  // hides no key; differences with it stay within 32 bits
   const size_t smem = 1024 + 4 * PA_Q_BYTES + (size_t)PA_SLOTS * PA_KV_BYTES + sizeof(PaSmall);
   cudaError_t err = cudaFuncSetAttribute(prompt_attn_sm100_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return set_error(CSLC_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(err));

@@ -253,6 +253,13 @@ def test_prompt_window(C, window):
     run_prompt(C, [290, 40], [290, 170], 8, 2, window=window, seed=window % 97)
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 129])
+def test_prompt_largest_window(C, window):
+    """The difference of a query without a key and the window stays within 32 bits."""
+    run_prompt(C, [200, 70, 300, 4], [73, 0, 299, 4], 8, 2, window=window, seed=11)
+    run_prompt(C, [150] * 90, [1, 0, 150] * 30, 4, 2, window=window, seed=12)
+
+
 def test_prompt_rows_of_no_sequence(C):
     run_prompt(C, [40, 3], [40, 60], 8, 2, lead=5, tail=21, seed=3)
     run_prompt(C, [0, 0], [4, 0], 4, 4, tail=130, seed=4)
