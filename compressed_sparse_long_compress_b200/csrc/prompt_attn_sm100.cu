@@ -27,7 +27,7 @@
 // would take 32 (it is bound by reading Q and K), but with 128 keys P has to lie
 // over S, and S of the next tile waits for P V of this one: 16.8 ms against 15.9.
 //
-// Measured (64 heads on 8, causal): 32,768 tokens 15.9 ms = 1,110 TFLOP/s at the
+// Measured (64 heads on 8, causal): 32,768 tokens 15.65 ms = 1,124 TFLOP/s at the
 // power limit (1,665 MHz; cuBLAS sustains 1,387 there), 8,192 tokens 1.05 ms. The
 // tensor-core pipe is busy 74 % of the cycles, the exponential pipe 56 %; without
 // any softmax arithmetic the same loop reaches 1,228 TFLOP/s. Exponentials moved
@@ -287,7 +287,7 @@ struct PaWs {
 __global__ void __launch_bounds__(PA_SCHED_THREADS) prompt_schedule_kernel(PaShape sh, const int32_t* __restrict__ cu_q,
                                                                            const int32_t* __restrict__ cu_k, PaWs ws) {
   extern __shared__ int pa_before[];             // [B + 1] pairs before sequence b
-  __shared__ int warp_sum_s[PA_SCHED_THREADS / 32];
+  __shared__ long long warp_sum_s[PA_SCHED_THREADS / 32];   // 64 bits: sequences that overlap count twice
   __shared__ int bucket[PA_BUCKETS];
   __shared__ int most_s;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");   // the attention's CTAs set up meanwhile
@@ -295,17 +295,18 @@ __global__ void __launch_bounds__(PA_SCHED_THREADS) prompt_schedule_kernel(PaSha
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int each = (sh.B + PA_SCHED_THREADS - 1) / PA_SCHED_THREADS;
   const int b0 = min(sh.B, tid * each), b1 = min(sh.B, b0 + each);
-  int sum = 0, most = 0;
+  long long sum = 0;
+  int most = 0;
   for (int b = b0; b < b1; ++b) {
     int q0, nq, k0, nk;
     pa_seq(sh, cu_q, cu_k, b, q0, nq, k0, nk);
     sum += pa_pairs(sh, nq);
     most = max(most, (nk + PA_KEYS - 1) / PA_KEYS);
   }
-  int incl = sum;
+  long long incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
   if (lane == 31) warp_sum_s[warp] = incl;
@@ -314,14 +315,14 @@ __global__ void __launch_bounds__(PA_SCHED_THREADS) prompt_schedule_kernel(PaSha
   __syncthreads();
   atomicMax(&most_s, most);
   for (int w = 0; w < warp; ++w) incl += warp_sum_s[w];
-  int at = incl - sum;
+  long long at = incl - sum;
   for (int b = b0; b < b1; ++b) {
-    pa_before[b] = at;
+    pa_before[b] = (int)min(at, 0x7fffffffll);
     int q0, nq, k0, nk;
     pa_seq(sh, cu_q, cu_k, b, q0, nq, k0, nk);
     at += pa_pairs(sh, nq);
   }
-  if (b0 < sh.B && b1 == sh.B) pa_before[sh.B] = at;
+  if (b0 < sh.B && b1 == sh.B) pa_before[sh.B] = (int)min(at, 0x7fffffffll);
   __syncthreads();
   const int n = min(pa_before[sh.B], ws.cap);     // more only where cu_q is not ascending
   // bucket 0: the most key tiles (with a window never more than the window and a pair's tokens span)
