@@ -541,6 +541,16 @@ static cslc_status check_stride(const char* fn, const char* what, long long stri
   return CSLC_OK;
 }
 
+// Do `an` bytes at a and `bn` bytes at b overlap?
+static bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x != 0 && y != 0 && an > 0 && bn > 0 && x < y + bn && y < x + an;
+}
+// Bytes from the first to the last element of n rows of heads, `stride` elements apart.
+static size_t rows_bytes(int n, int heads, long long stride) {
+  return n <= 0 ? 0 : ((size_t)(n - 1) * stride + (size_t)heads * kD) * sizeof(uint16_t);
+}
+
 #define FORWARD(call)                          \
   do {                                         \
     const cslc_status st_ = (call);            \
@@ -560,6 +570,14 @@ cslc_status cslc_page_plan(const int32_t* old_len, const int32_t* new_len, int B
   }
   if (n_free > 0) REQUIRE_PTR(free_pages);
   if (max_tokens > 0) REQUIRE_PTR(slots);
+  // other CTAs still read the inputs when one writes its results
+  const size_t w = sizeof(int32_t);
+  const struct { const void* p; size_t n; } in[3] = {{old_len, B * w}, {new_len, B * w}, {free_pages, n_free * w}},
+      res[5] = {{block_table, (size_t)B * max_pages * w}, {slots, max_tokens * w}, {cu, (B + 1) * w}, {seq_len, B * w},
+                {status, 2 * w}};
+  for (const auto& i : in)
+    for (const auto& r : res)
+      REQUIRE(!overlap(i.p, i.n, r.p, r.n), CSLC_ERR_UNSUPPORTED, "cslc_page_plan: a result overlaps an input");
   return launch_page_plan(old_len, new_len, B, free_pages, n_free, page, n_pages, max_pages, max_tokens, block_table,
                           slots, cu, seq_len, status, stream);
 }
@@ -597,7 +615,7 @@ cslc_status cslc_prompt_attn(const cslc_bf16* q, const cslc_bf16* k, const cslc_
   FORWARD(check_stride(fn, "q_stride", q_stride, H));
   FORWARD(check_stride(fn, "k_stride", k_stride, Hkv));
   FORWARD(check_stride(fn, "v_stride", v_stride, Hkv));
-  REQUIRE(scale > 0.f && scale <= 3.402823466e38f, CSLC_ERR_UNSUPPORTED, "%s: scale must be positive and finite", fn);
+  REQUIRE(scale > 0.f && scale * kLog2e <= 3.402823466e38f, CSLC_ERR_UNSUPPORTED, "%s: scale must be positive and finite", fn);
   REQUIRE((long long)Tq * H < (1ll << 31) && (long long)Tk * Hkv < (1ll << 31), CSLC_ERR_UNSUPPORTED,
           "%s: Tq * H and Tk * H_kv must be below 2^31", fn);
   if (B == 0 || Tq == 0) return CSLC_OK;
@@ -608,6 +626,10 @@ cslc_status cslc_prompt_attn(const cslc_bf16* q, const cslc_bf16* k, const cslc_
   REQUIRE(need == 0 || (ws != nullptr && ws_bytes >= need), CSLC_ERR_WORKSPACE, "%s: workspace of %zu bytes needed",
           fn, need);
   REQUIRE(aligned16(ws), CSLC_ERR_ALIGN, "%s: ws is not 16-byte aligned", fn);
+  const size_t out_n = rows_bytes(Tq, H, (long long)H * kD);
+  REQUIRE(!overlap(out, out_n, q, rows_bytes(Tq, H, q_stride)) && !overlap(out, out_n, k, rows_bytes(Tk, Hkv, k_stride)) &&
+              !overlap(out, out_n, v, rows_bytes(Tk, Hkv, v_stride)),
+          CSLC_ERR_UNSUPPORTED, "%s: out overlaps an input", fn);
   return launch_prompt_attn(q, k, v, cu_q, cu_k, B, Tq, Tk, H, Hkv, q_stride, k_stride, v_stride, window, scale, out,
                             lse, ws, stream);
 }
@@ -628,7 +650,7 @@ cslc_status cslc_page_decode_attn(const cslc_bf16* q, const uint8_t* k_cache, co
   FORWARD(check_heads(fn, H, Hkv, D));
   FORWARD(check_pages(fn, Hkv, page, n_pages));
   FORWARD(check_stride(fn, "q_stride", q_stride, H));
-  REQUIRE(scale > 0.f && scale <= 3.402823466e38f, CSLC_ERR_UNSUPPORTED, "%s: scale must be positive and finite", fn);
+  REQUIRE(scale > 0.f && scale * kLog2e <= 3.402823466e38f, CSLC_ERR_UNSUPPORTED, "%s: scale must be positive and finite", fn);
   if (B == 0) return CSLC_OK;
   REQUIRE_PTR(q); REQUIRE_PTR(seq_len); REQUIRE_PTR(out);
   if (max_pages > 0) REQUIRE_PTR(block_table);
@@ -638,6 +660,8 @@ cslc_status cslc_page_decode_attn(const cslc_bf16* q, const uint8_t* k_cache, co
   REQUIRE(need == 0 || (ws != nullptr && ws_bytes >= need), CSLC_ERR_WORKSPACE, "%s: workspace of %zu bytes needed",
           fn, need);
   REQUIRE(aligned16(ws), CSLC_ERR_ALIGN, "%s: ws is not 16-byte aligned", fn);
+  REQUIRE(!overlap(out, rows_bytes(B, H, (long long)H * kD), q, rows_bytes(B, H, q_stride)), CSLC_ERR_UNSUPPORTED,
+          "%s: out overlaps q", fn);
   return launch_page_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len, B, H, Hkv, page, n_pages,
                             max_pages, q_stride, window, scale, out, lse, ws, stream);
 }

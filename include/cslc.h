@@ -22,7 +22,8 @@
  *     where it is loaded, until the process exits; only
  *     cslc_decode_topk_noalloc (at the end of this header) uses it.
  *   - Tensors are dense, row-major (last index fastest) with the shapes given
- *     below. bf16 tensors are passed as cslc_bf16 (raw bfloat16 bits).
+ *     below; the paged entry points take a row stride for some. bf16 tensors
+ *     are passed as cslc_bf16 (raw bfloat16 bits).
  *     Every pointer must be 16-byte aligned (CSLC_ERR_ALIGN otherwise).
  *   - Calls are asynchronous on `stream` (NULL = the legacy default stream) and
  *     return after the launches are enqueued. Arguments are validated before
@@ -33,7 +34,8 @@
  *   - Supported shapes: D = 128 (compressed entry / head dim), d_I = 64, H a
  *     multiple of 16 up to 128, H_I <= 16, 1 <= topk <= 2048, m a power of two
  *     in [1, 128] for compression (any m >= 1 for visibility). Anything else
- *     returns CSLC_ERR_UNSUPPORTED.
+ *     returns CSLC_ERR_UNSUPPORTED. (The paged entry points have head counts
+ *     of their own.)
  *
  * Geometry shared by every call (the pages leave it open; this is the reading
  * the library follows): entry i of a compression with ratio m covers the
@@ -400,7 +402,7 @@ cslc_status cslc_decode_topk(const float* scores, const int32_t* n_entries, int 
  *   status [2] int32: pages handed out (more than n_free when the list was too
  *       short), and new tokens that have no page (0 when all went well)
  * 0 <= B <= 8192. The caller takes the first status[0] pages off its list.
- * One launch; no workspace. */
+ * No result may overlap old_len, new_len or free_pages. One launch; no workspace. */
 cslc_status cslc_page_plan(const int32_t* old_len, const int32_t* new_len, int B, const int32_t* free_pages,
                            int n_free, int page, int n_pages, int max_pages, int max_tokens,
                            int32_t* block_table, int32_t* slots, int32_t* cu, int32_t* seq_len,
@@ -451,7 +453,8 @@ cslc_status cslc_page_write_e4m3(const cslc_bf16* k, const cslc_bf16* v, const i
  *   out [Tq, H, 128] bf16; lse [Tq, H] fp32 (natural log-sum-exp), or NULL
  *   ws  workspace of cslc_prompt_attn_workspace_bytes() bytes; it belongs to
  *       one call at a time (also in captured graphs)
- * 0 <= B <= 8192, window >= 0, scale positive and finite. */
+ * (ws may be NULL where that is 0). out may not overlap an input.
+ * 0 <= B <= 8192, window >= 0; scale is positive and scale * log2(e) finite. */
 size_t cslc_prompt_attn_workspace_bytes(int B, int Tq, int H, int Hkv);
 cslc_status cslc_prompt_attn(const cslc_bf16* q, const cslc_bf16* k, const cslc_bf16* v, const int32_t* cu_q,
                              const int32_t* cu_k, int B, int Tq, int Tk, int H, int Hkv, int D, int64_t q_stride,
@@ -471,7 +474,8 @@ cslc_status cslc_prompt_attn(const cslc_bf16* q, const cslc_bf16* k, const cslc_
  *   out [B, H, 128] bf16; lse [B, H] fp32, or NULL
  *   ws  workspace of cslc_page_decode_workspace_bytes() bytes; it belongs to
  *       one call at a time (also in captured graphs)
- * 0 <= B <= 8192, window >= 0, scale positive and finite. */
+ * out may not overlap q. 0 <= B <= 8192, window >= 0; scale is positive and
+ * scale * log2(e) finite. */
 size_t cslc_page_decode_workspace_bytes(int B, int H, int Hkv);
 cslc_status cslc_page_decode_attn(const cslc_bf16* q, const uint8_t* k_cache, const uint8_t* v_cache,
                                   const float* k_scale, const float* v_scale, const int32_t* block_table,

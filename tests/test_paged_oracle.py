@@ -174,6 +174,31 @@ def test_decode_refusals():
         assert _decode(ws=None, nws=0)[0] == 5 and _decode(nws=1)[0] == 5
 
 
+def test_results_over_inputs_are_refused():
+    at0, n = 1 << 30, 1 << 20                                  # n: bytes between pointers that do not overlap
+    far = dict(zip(("old", "new", "free", "table", "slots", "cu", "len", "status"), (at0 + i * n for i in range(8))))
+    for res, size in (("table", 12), ("slots", 40), ("cu", 3), ("len", 2), ("status", 2)):
+        for inp, count in (("old", 2), ("new", 2), ("free", 4)):
+            for at in (far[inp], far[inp] - (size * 4 - 1) // 16 * 16):
+                a = dict(far, **{res: at})
+                st, msg = _err(cslc.LIB.cslc_page_plan(a["old"], a["new"], 2, a["free"], count, 16, 9, 6, 40, a["table"],
+                                                       a["slots"], a["cu"], a["len"], a["status"], None))
+                assert st == 4 and "overlaps" in msg, (res, inp)
+    for out in (at0, at0 + 7 * 2048, at0 + n + 16, at0 + 2 * n - 16):
+        a = dict(q=at0, k=at0 + n, v=at0 + 2 * n, out=out)
+        st, msg = _prompt(**a)
+        assert st == 4 and "overlaps" in msg, out
+    for out in (at0, at0 + 1024 * 2, at0 - 16):
+        st, msg = _decode(q=at0, out=out)
+        assert st == 4 and "overlaps" in msg
+
+
+def test_scales_beyond_fp32_are_refused():
+    for scale in (0.0, -1.0, float("nan"), float("inf"), 3e38):
+        assert _prompt(scale=scale, out=1 << 30)[0] == 4
+        assert _decode(scale=scale, out=1 << 30)[0] == 4
+
+
 def test_workspace_of_head_counts_that_are_refused():
     """The binding asks for the size before the call checks its arguments."""
     for H, Hkv in ((256, 1), (129, 1), (1 << 20, 1), (0, 1), (8, 0), (8, 3), (-8, 1), (8, -1)):
