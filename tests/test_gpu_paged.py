@@ -705,6 +705,51 @@ def test_write_rows_far_apart(C):
         C.page_write_e4m3(big[:, 1:5:2], big[:, 1:3], i32(range(20, 70)), kc, vc, ks, vs)
 
 
+@pytest.mark.parametrize("P,Hkv", [(128, 8), (16, 5)])
+def test_cache_beyond_32_bits(C, P, Hkv):
+    """Pages whose codes lie more than 2^32 bytes into the cache: written, and read by the decode attention."""
+    n_pages = (2 ** 32 + 2 ** 30) // (Hkv * P * 128)
+    first, last = [0, 5, 2], [n_pages - 1, n_pages - 70, n_pages * 7 // 8, n_pages // 2 + 1]
+    pages = last + first                                       # the sequence's pages, in order
+    kc, vc = (torch.empty((n_pages, Hkv, P, 128), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.empty((n_pages, Hkv), device="cuda") for _ in range(2))
+    at = i32(pages).long()
+    for c in (kc, vc):
+        c[at] = 0x7F
+    for c in (ks, vs):
+        c[at] = 2.0 ** -9
+    n = len(pages) * P - 5
+    k, v = randn((n, Hkv, 128), 21), randn((n, Hkv, 128), 22)
+    small = [c[at].cpu().numpy() for c in (kc, vc)]
+    C.page_write_e4m3(k, v, i32([pages[x // P] * P + x % P for x in range(n)]), kc, vc, ks, vs)
+    C.sync_status()
+    near = []
+    for x, c, sc, (cache, scale) in ((k, small[0], ks, (kc, ks)), (v, small[1], vs, (vc, vs))):
+        codes, ref = PO.page_write(f64(x), np.arange(n), c, np.full((len(pages), Hkv), 2.0 ** -9))
+        assert np.array_equal(cache[at].cpu().numpy(), codes) and np.array_equal(f64(scale[at]), ref)
+        near.append((codes, ref))
+    lens = [n, 2 * P + 3]
+    q = randn((2, 2 * Hkv, 128), 23)
+    out, lse = C.page_decode_attn(q, kc, vc, ks, vs, i32([pages, pages]), i32(lens), SCALE, lse=True)
+    C.sync_status()
+    table = np.tile(np.arange(len(pages)), (2, 1))
+    check_attention(out, lse, PO.page_decode_attention(f64(q), near[0][0], near[1][0], near[0][1], near[1][1], table, lens, SCALE),
+                    n, "far pages")
+
+
+def test_prompt_rows_beyond_32_bits(C):
+    """Rows of q, k and v that lie up to 5 GB apart."""
+    T, H, Hkv = 600, 4, 2
+    big = torch.empty((T, 2 ** 22), dtype=BF16, device="cuda")
+    q, k, v = (big[:, c * 2 ** 20:c * 2 ** 20 + h * 128].unflatten(1, (h, 128)) for c, h in ((0, H), (1, Hkv), (3, Hkv)))
+    for i, x in enumerate((q, k, v)):
+        x.copy_(randn(x.shape, 30 + i))
+    cu = [0, 170, T]
+    out, lse = C.prompt_attn(q, k, v, i32(cu), i32(cu), SCALE, lse=True)
+    C.sync_status()
+    check_attention(out, lse, PO.prompt_attention(f64(q), f64(k), f64(v), cu, cu, SCALE), 430, "far rows")
+
+
 def test_binding_refusals_on_the_device(C):
     q, k = randn((4, 8, 128), 1), randn((4, 2, 128), 2)
     cu = i32([0, 4])
