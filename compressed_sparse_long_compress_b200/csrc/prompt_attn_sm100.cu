@@ -27,9 +27,9 @@
 // would take 32 (it is bound by reading Q and K), but with 128 keys P has to lie
 // over S, and S of the next tile waits for P V of this one: 16.8 ms against 15.9.
 //
-// Measured (64 heads on 8, causal): 32,768 tokens 15.65 ms = 1,124 TFLOP/s at the
-// power limit (1,665 MHz; cuBLAS sustains 1,387 there), 8,192 tokens 1.05 ms. The
-// tensor-core pipe is busy 74 % of the cycles, the exponential pipe 56 %; without
+// Measured (64 heads on 8, causal): 32,768 tokens 15.4 ms = 1,143 TFLOP/s at the
+// power limit (1,665 MHz; cuBLAS sustains 1,387 there), 8,192 tokens 1.00 ms. The
+// tensor-core pipe is busy 78 % of the cycles, the exponential pipe 56 %; without
 // any softmax arithmetic the same loop reaches 1,228 TFLOP/s. Exponentials moved
 // to the FMA pipe by a polynomial, single instead of packed fp32 operations, and
 // one thread issuing the products were all slower: at the power limit every
@@ -37,8 +37,13 @@
 //
 // Order of work. prompt_schedule_kernel sorts the Q-tile pairs of all sequences
 // by their number of key tiles, largest first; the CTAs draw tickets, so ragged
-// and causal work evens out. The pairs of one key head are drawn together, so
-// that its keys and values stay in L2. Few items (at most one for each CTA)
+// and causal work evens out. The longer half of the pairs is drawn one key head
+// after the other, so that its keys and values stay in L2; the shorter half of all
+// heads comes last, longest first, and evens out what the long ones leave (all
+// pairs head by head left the SMs busy 93 % of the time at 8,192 tokens: 1.08 ms
+// against 1.00; all heads mixed 16.5 ms against 15.4 at 32,768). A CTA draws its next
+// item late, with six key tiles left to load: 4,096 tokens of 32 heads 173 -> 156 us.
+// Few items (at most one for each CTA)
 // need no order and no ticket: that saves the schedule's 5 us.
 //
 // A value that is masked for some row of a tile may be NaN or infinite, and
@@ -433,6 +438,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       };
       const int n_pairs = sh.direct ? 0 : ws.head[1];
       const long long n_items = (long long)n_pairs * sh.Hkv;
+      const int n_long = n_pairs / 2;                    // pairs drawn head by head
       auto fetch = [&](bool first) -> PaTake {           // the next item
         PaTake t;
         int b = -1, pair = 0;
@@ -451,10 +457,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         } else {
           const long long i = atomicAdd(ws.head, 1);
           if (i < n_items) {
-            const int2 bp = ws.list[i % n_pairs];
+            long long p = i - (long long)n_long * sh.Hkv;
+            if (p < 0) { p = i % n_long; t.hk = (int)(i / n_long); }
+            else { t.hk = (int)(p % sh.Hkv); p = n_long + p / sh.Hkv; }
+            const int2 bp = ws.list[p];
             b = bp.x;
             pair = bp.y;
-            t.hk = (int)(i / n_pairs);
           }
         }
         t.there = b >= 0;
@@ -480,14 +488,14 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
           tma_load_3d(dst, &tm_q, 0, hk * sh.G, tok, &bars.q_full[n & 1]);
           tma_load_3d(dst + PA_ROWS * 128, &tm_q, 64, hk * sh.G, tok, &bars.q_full[n & 1]);
         }
-        // in the order of use: K0 K1 V0 K2 V1 .. The next item is looked up behind the first tiles.
+        // in the order of use: K0 K1 V0 K2 V1 .. The next item is looked up with the last tiles in front of it.
         if (it.jb < it.je) ok = load_tile(&tm_k, hk, it.k0 + it.jb * PA_KEYS);
         if (ok && it.jb + 1 < it.je) ok = load_tile(&tm_k, hk, it.k0 + (it.jb + 1) * PA_KEYS);
         bool fetched = false;
         for (int j = it.jb; j < it.je && ok; ++j) {
           ok = load_tile(&tm_v, hk, it.k0 + j * PA_KEYS);
           if (ok && j + 2 < it.je) ok = load_tile(&tm_k, hk, it.k0 + (j + 2) * PA_KEYS);
-          if (j == it.jb + 1) { next = fetch(false); fetched = true; }
+          if (!fetched && j > it.jb && j + 6 >= it.je) { next = fetch(false); fetched = true; }
         }
         if (!ok) break;
         if (!fetched) next = fetch(false);
