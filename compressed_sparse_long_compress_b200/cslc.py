@@ -618,12 +618,13 @@ def prompt_attn(q, k, v, cu_q, cu_k, scale: float, window: int = 0, out=None, ls
         lse = _alloc((Tq, H), F32, dev, stream)
     pl = None if lse is None else _at(lse, F32, "lse", dev, (Tq, H))
     if ws is None:
-        n_ws = LIB.cslc_prompt_attn_workspace_bytes(B, Tq, H, Hkv)
+        n_ws, p_ws = LIB.cslc_prompt_attn_workspace_bytes(B, Tq, H, Hkv), None
         if n_ws:
             ws = _alloc((n_ws,), U8, dev, stream)
+            p_ws = ws.data_ptr()
     else:
         n_ws = ws.numel()
-    p_ws = None if ws is None else _at(ws, U8, "ws", dev, (n_ws,))
+        p_ws = _at(ws, U8, "ws", dev, (n_ws,))
     _run_on(dev, stream, LIB.cslc_prompt_attn, pq, pk, pv, p_cu_q, p_cu_k, B, Tq, Tk, H, Hkv, D, qs, ks, vs, window, scale,
             po, pl, p_ws, n_ws)
     return out, lse
@@ -654,9 +655,12 @@ def page_decode_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
         lse = _alloc((B, H), F32, dev, stream)
     pl = None if lse is None else _at(lse, F32, "lse", dev, (B, H))
     if ws is None:
-        nbytes = LIB.cslc_page_decode_workspace_bytes(B, H, Hkv)
-        ws = _alloc((nbytes,), U8, dev, stream)
-    n_ws = ws.numel()
+        n_ws = LIB.cslc_page_decode_workspace_bytes(B, H, Hkv)
+        ws = _alloc((n_ws,), U8, dev, stream)
+        p_ws = ws.data_ptr()
+    else:
+        n_ws = ws.numel()
+        p_ws = _at(ws, U8, "ws", dev, (n_ws,))
     _run_on(dev, stream, LIB.cslc_page_decode_attn, pq, pkc, pvc, pks, pvs, p_table, p_len, B, H, Hkv, D, P, n_pages,
-            max_pages, qs, window, scale, po, pl, _at(ws, U8, "ws", dev, (n_ws,)), n_ws)
+            max_pages, qs, window, scale, po, pl, p_ws, n_ws)
     return out, lse
