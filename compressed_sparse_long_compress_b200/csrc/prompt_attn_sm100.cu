@@ -17,7 +17,7 @@
 //                   as bf16 (off by at most 2^-8 of itself) and is the A operand
 //                   of P V from there: no shared memory and no proxy fence.
 //   warp 8          producer: Q tiles (two items), K and V tiles of 64 keys
-//                   (TMA, 6-deep ring of 16 KB)
+//                   (TMA, 6-deep ring of 16 KB); stores whole tiles of results
 //   warps 9, 10     MMA issue for Q tile 0 and 1 (9 also allocates TMEM): S of
 //                   the next tile as soon as this tile's scores are in
 //                   registers, P V of this tile when P is there. So a softmax
@@ -27,8 +27,8 @@
 // would take 32 (it is bound by reading Q and K), but with 128 keys P has to lie
 // over S, and S of the next tile waits for P V of this one: 16.8 ms against 15.9.
 //
-// Measured (64 heads on 8, causal): 32,768 tokens 15.4 ms = 1,143 TFLOP/s at the
-// power limit (1,665 MHz; cuBLAS sustains 1,387 there), 8,192 tokens 1.00 ms. The
+// Measured (64 heads on 8, causal): 32,768 tokens 15.5 ms = 1,135 TFLOP/s at the
+// power limit (1,665 MHz; cuBLAS sustains 1,387 there), 8,192 tokens 1.02 ms. The
 // tensor-core pipe is busy 78 % of the cycles, the exponential pipe 56 %; without
 // any softmax arithmetic the same loop reaches 1,228 TFLOP/s. Exponentials moved
 // to the FMA pipe by a polynomial, single instead of packed fp32 operations, and
@@ -74,6 +74,8 @@ constexpr int PA_KV_BYTES = PA_KEYS * 256;
 constexpr int PA_KV_HALF = PA_KEYS * 128;
 constexpr float PA_SUM_MAX = 65536.f;            // values of up to 2^111 do not overflow O
 constexpr int PA_SMS = 148;
+constexpr int PA_APART = 450;                    // cycles between the Q tiles' softmaxes, in items of more
+constexpr int PA_APART_MIN = 12;                 // key tiles than this
 constexpr int PA_BUCKETS = 512;
 constexpr int PA_SCHED_THREADS = 1024;
 
@@ -165,6 +167,16 @@ __device__ __forceinline__ void tmem_wait_ld64(uint32_t (&r)[2][32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[0][i]), "+r"(r[1][i]));
 }
+// A box of shared memory into the tensor of `map`, and the waits for a thread's own stores: until
+// they have read their source, and until they are done.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];\n" ::"l"(map),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store_commit() { asm volatile("cp.async.bulk.commit_group;\n" ::: "memory"); }
+__device__ __forceinline__ void bulk_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+__device__ __forceinline__ void bulk_store_wait() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -266,7 +278,9 @@ __device__ __noinline__ void pa_slow_pv(uint32_t t_o, uint32_t t_p, const uint8_
   tmem_wait_st();
 }
 // A warp's rows r0 .. r0 + 31 of a tile, those below `full`, from there to `dst` (the tile's first row).
+// A whole tile is left to the producer's TMA.
 __device__ __noinline__ void pa_store_rows(uint16_t* dst, const uint8_t* stage, int r0, int full, int G, int H, int inv_g) {
+  if (PA_ROWS - full < G) return;
   const int lane = threadIdx.x & 31, c = lane & 15;
 #pragma unroll 4
   for (int i = 0; i < 16; ++i) {
@@ -375,7 +389,7 @@ __global__ void __launch_bounds__(PA_SCHED_THREADS) prompt_schedule_kernel(PaSha
 __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
     PaShape sh, const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k, PaWs ws, uint16_t* __restrict__ out,
     float* __restrict__ lse, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-    const __grid_constant__ CUtensorMap tm_v) {
+    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_s = smem;                                   // [2 items][2 tiles][2 halves][128][128 B]
@@ -469,16 +483,42 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         if (b >= 0) t.it = pa_item(sh, cu_q, cu_k, b, pair);
         return t;
       };
+      // Whole Q tiles' results are stored from their place in the Q tile when that is to be loaded again, an
+      // item later: the softmax warps' own stores took 2,300 of the 22,600 cycles of an item of ten key tiles.
+      int o_tok[2], o_hk[2], o_n[2][2];                  // by item parity: first token, key head, tokens by Q tile
+      auto store_out = [&](int i) -> bool {
+        if (!mbar_wait(&bars.q_empty[i & 1], (uint32_t)((i >> 1) & 1), abortp, errp, PA_ERR_Q_EMPTY)) return false;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const int o = (i & 1) ? o_n[1][w] : o_n[0][w], hk = (i & 1) ? o_hk[1] : o_hk[0];
+          if (o < sh.tpt) continue;
+          const int tok = ((i & 1) ? o_tok[1] : o_tok[0]) + w * sh.tpt;
+          const uint8_t* src = q_s + ((i & 1) * 2 + w) * PA_Q_BYTES;
+          tma_store_3d(&tm_o, src, 0, hk * sh.G, tok);
+          tma_store_3d(&tm_o, src + PA_ROWS * 128, 64, hk * sh.G, tok);
+        }
+        bulk_store_commit();
+        return true;
+      };
       PaTake next = fetch(true);
       for (;; ++n) {
         const PaTake t = next;
         if (n >= 2 && !mbar_wait(&bars.item_empty[n & 1], (uint32_t)(((n >> 1) - 1) & 1), abortp, errp, PA_ERR_ITEM)) break;
         sm->take[n & 1] = t;
         mbar_arrive(&bars.item_full[n & 1]);
-        if (!t.there) break;
+        if (!t.there) {
+          if (n >= 2 && !store_out(n - 2)) break;
+          if (n >= 1) store_out(n - 1);
+          break;
+        }
         const PaItem& it = t.it;
         const int hk = t.hk;
-        if (n >= 2 && !mbar_wait(&bars.q_empty[n & 1], (uint32_t)(((n >> 1) - 1) & 1), abortp, errp, PA_ERR_Q_EMPTY)) break;
+        if (n >= 2) {
+          if (!store_out(n - 2)) break;
+          bulk_store_wait_read();
+        }
+        if (n & 1) { o_tok[1] = it.q0 + it.t0; o_hk[1] = hk; o_n[1][0] = it.n[0]; o_n[1][1] = it.n[1]; }
+        else { o_tok[0] = it.q0 + it.t0; o_hk[0] = hk; o_n[0][0] = it.n[0]; o_n[0][1] = it.n[1]; }
         q_loads = n + 1;
         mbar_arrive_expect_tx(&bars.q_full[n & 1], (uint32_t)(4 * rows * 128));
 #pragma unroll
@@ -500,6 +540,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         if (!ok) break;
         if (!fetched) next = fetch(false);
       }
+      bulk_store_wait();
       // loads in flight after an abort land before the CTA leaves
       for (int d = 1; d <= 2 && q_loads - d >= 0; ++d)
         mbar_wait_done(&bars.q_full[(q_loads - d) & 1], (uint32_t)(((q_loads - d) >> 1) & 1), errp, PA_ERR_Q_FULL);
@@ -665,6 +706,13 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         // (the PV of two tiles before, which read this tile's P buffer, was issued before these
         // scores, so it is done too)
         tc_fence_after();
+        // An item's two softmaxes keep the distance that they start with, and run best a third of a tile apart,
+        // where one loads scores while the other has the exponentials: 8,192 tokens 1.077 ms with 200 cycles,
+        // 1.013 with 400 to 500, 1.022 with 600, 1.05 with 0 or 900. A short item would not earn the wait.
+        if (w == 0 && j == j0 && j1 - j0 > PA_APART_MIN) {
+          const long long t0 = clock64();
+          while (clock64() - t0 < PA_APART) {}
+        }
         uint32_t s[2][32];
         auto at = [&](int k) { return __uint_as_float(s[k >> 5][k & 31]); };
         tmem_ld32(t_s, s[0]);
@@ -768,8 +816,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
                 : wait(&bars.q_full[n & 1], (uint32_t)((n >> 1) & 1), PA_ERR_Q_FULL)))
         break;
       tc_fence_after();
-      // The warp's 32 rows go through the item's Q tile, which every S has read, so that the stores
-      // are whole rows (16 bytes of 32 rows in one store took 4,100 to 5,200 cycles an item).
+      // The warp's 32 rows go through the item's Q tile, which every S has read, so that the stores are whole
+      // rows (16 bytes of 32 rows in one store took 4,100 to 5,200 cycles an item) or the producer's.
       const float inv = l == 0.f ? 0.f : 1.f / l;
       uint8_t* stage = q_s + ((n & 1) * 2 + w) * PA_Q_BYTES;
       pa_stage_rows(t_o, stage, row < rows ? row : -1, any, l == 0.f, inv);
@@ -829,11 +877,12 @@ cslc_status launch_prompt_attn(const uint16_t* q, const uint16_t* k, const uint1
   const int G = H / Hkv, tpt = PA_ROWS / G;
   const long long items = pa_most_pairs(B, Tq, tpt) * Hkv;
   const PaShape sh{B, Tq, Tk, H, Hkv, G, tpt, window, scale, scale * kLog2e, pa_direct(B, Tq, H, Hkv) ? 1 : 0};
-  CUtensorMap tm_q, tm_k, tm_v;
+  CUtensorMap tm_q, tm_k, tm_v, tm_o;
   // without keys no tile of them is loaded: the maps only have to be valid
   const bool keys = Tk > 0;
   if (!make_tmap_bf16_rows128(&tm_q, q, H, Tq, q_stride, G, tpt) ||
       !make_tmap_bf16_rows128(&tm_k, keys ? k : q, keys ? Hkv : H, keys ? Tk : Tq, keys ? k_stride : q_stride, 1, PA_KEYS) ||
+      !make_tmap_bf16_rows128(&tm_o, out, H, Tq, (long long)H * kD, G, tpt) ||
       !make_tmap_bf16_rows128(&tm_v, keys ? v : q, keys ? Hkv : H, keys ? Tk : Tq, keys ? v_stride : q_stride, 1, PA_KEYS))
     return set_error(CSLC_ERR_CUDA, "%s: tensor map encoding failed", fn);
   PaWs ws;
@@ -846,7 +895,7 @@ cslc_status launch_prompt_attn(const uint16_t* q, const uint16_t* k, const uint1
     if (err != cudaSuccess) return set_error(CSLC_ERR_CUDA, "prompt_schedule_kernel: %s", cudaGetErrorString(err));
   }
   err = launch_after(prompt_attn_sm100_kernel, dim3((unsigned)(items < PA_SMS ? items : PA_SMS)), dim3(PA_THREADS), smem,
-                         stream, sh, cu_q, cu_k, ws, out, lse, tm_q, tm_k, tm_v);
+                         stream, sh, cu_q, cu_k, ws, out, lse, tm_q, tm_k, tm_v, tm_o);
   if (err != cudaSuccess) return set_error(CSLC_ERR_CUDA, "prompt_attn_sm100_kernel: %s", cudaGetErrorString(err));
   return CSLC_OK;
 }
