@@ -27,8 +27,8 @@
 // would take 32 (it is bound by reading Q and K), but with 128 keys P has to lie
 // over S, and S of the next tile waits for P V of this one: 16.8 ms against 15.9.
 //
-// Measured (64 heads on 8, causal): 32,768 tokens 15.5 ms = 1,135 TFLOP/s at the
-// power limit (1,665 MHz; cuBLAS sustains 1,387 there), 8,192 tokens 1.02 ms. The
+// Measured (64 heads on 8, causal): 32,768 tokens 15.4 ms = 1,142 TFLOP/s at the
+// power limit (1,665 MHz; cuBLAS sustains 1,387 there), 8,192 tokens 1.01 ms. The
 // tensor-core pipe is busy 78 % of the cycles, the exponential pipe 56 %; without
 // any softmax arithmetic the same loop reaches 1,228 TFLOP/s. Exponentials moved
 // to the FMA pipe by a polynomial, single instead of packed fp32 operations, and
@@ -202,6 +202,14 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
   return r;
 }
 
+// mbar_wait with the part that really waits out of line. The kernel's code competes for the instruction cache:
+// a dozen inlined waits cost 3 % of 17 ragged prompts and 6 % of 100 short ones; unrolled staging cost 11 % of those.
+__device__ __noinline__ bool pa_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int code) {
+  return mbar_wait(bar, parity, abort, err, code);
+}
+__device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int code) {
+  return mbar_test(bar, parity) || pa_wait_slow(bar, parity, abort, err, code);
+}
 // Out of line: their registers and code stay out of the softmax loop's.
 // A row of O (none of it: zeros) through 1 / l into its place of the Q tile, row -1: nothing.
 __device__ __noinline__ void pa_stage_rows(uint32_t t_o, uint8_t* stage, int row, bool any, bool nothing, float inv) {
@@ -441,7 +449,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       auto load_tile = [&](const CUtensorMap* map, int hk, int row) -> bool {
         const int s = kv % PA_SLOTS;
         if (kv >= PA_SLOTS &&
-            !mbar_wait(&bars.empty[s], (uint32_t)((kv / PA_SLOTS - 1) & 1), abortp, errp, PA_ERR_EMPTY))
+            !pa_wait(&bars.empty[s], (uint32_t)((kv / PA_SLOTS - 1) & 1), abortp, errp, PA_ERR_EMPTY))
           return false;
         uint8_t* dst = ring + s * PA_KV_BYTES;
         mbar_arrive_expect_tx(&bars.full[s], PA_KV_BYTES);
@@ -487,7 +495,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       // item later: the softmax warps' own stores took 2,300 of the 22,600 cycles of an item of ten key tiles.
       int o_tok[2], o_hk[2], o_n[2][2];                  // by item parity: first token, key head, tokens by Q tile
       auto store_out = [&](int i) -> bool {
-        if (!mbar_wait(&bars.q_empty[i & 1], (uint32_t)((i >> 1) & 1), abortp, errp, PA_ERR_Q_EMPTY)) return false;
+        if (!pa_wait(&bars.q_empty[i & 1], (uint32_t)((i >> 1) & 1), abortp, errp, PA_ERR_Q_EMPTY)) return false;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const int o = (i & 1) ? o_n[1][w] : o_n[0][w], hk = (i & 1) ? o_hk[1] : o_hk[0];
@@ -503,7 +511,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       PaTake next = fetch(true);
       for (;; ++n) {
         const PaTake t = next;
-        if (n >= 2 && !mbar_wait(&bars.item_empty[n & 1], (uint32_t)(((n >> 1) - 1) & 1), abortp, errp, PA_ERR_ITEM)) break;
+        if (n >= 2 && !pa_wait(&bars.item_empty[n & 1], (uint32_t)(((n >> 1) - 1) & 1), abortp, errp, PA_ERR_ITEM)) break;
         sm->take[n & 1] = t;
         mbar_arrive(&bars.item_full[n & 1]);
         if (!t.there) {
@@ -664,6 +672,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abortp, errp, code));
     };
+    auto wait_out = [&](uint64_t* bar, uint32_t parity, int code) -> bool {
+      if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+      return __all_sync(0xffffffffu, pa_wait_slow(bar, parity, abortp, errp, code));
+    };
     // is the V tile at ring position vv finite? Two threads to a key; a warp finds out about its 16
     auto scan_v = [&](int vv, bool& bad) -> bool {
       const int vs = vv % PA_SLOTS, key = row >> 1;
@@ -682,7 +694,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
     };
     const int ti = row / sh.G, inv_g = 65535 / sh.G + 1; // this row's token of the Q tile; r / G = r inv_g >> 16
     for (int n = 0; ok; ++n) {
-      if (!wait(&bars.item_full[n & 1], (uint32_t)((n >> 1) & 1), PA_ERR_ITEM)) break;
+      if (!wait_out(&bars.item_full[n & 1], (uint32_t)((n >> 1) & 1), PA_ERR_ITEM)) break;
       if (!sm->take[n & 1].there) break;
       const PaItem& it = sm->take[n & 1].it;             // stays there until the tile is done
       const int tw = it.t0 + w * sh.tpt;                 // the Q tile's first token
@@ -702,7 +714,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         const bool part = j < whole0 || j >= whole1;
         // ring position of its V: behind the K of up to two tiles more
         auto vv = [&]() { return kv0 + (j - it.jb) + min(j - it.jb + 2, it.je - it.jb); };
-        if (!wait(&bars.s_full[w], (uint32_t)(t_it & 1), PA_ERR_S_FULL)) { ok = false; break; }
+        if (!wait_out(&bars.s_full[w], (uint32_t)(t_it & 1), PA_ERR_S_FULL)) { ok = false; break; }
         // (the PV of two tiles before, which read this tile's P buffer, was issued before these
         // scores, so it is done too)
         tc_fence_after();
@@ -723,14 +735,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         if (lane == 0) mbar_arrive(&bars.s_read[w]);
         if (part) {
           const int hi = row_ok ? last + 1 - j * PA_KEYS : PA_KEYS, l0 = row_ok ? lo - j * PA_KEYS : 0;
-          if (j >= whole1) {
+          // one select for each key, by a bit: two passes of compares were 2 to 3 % slower in all
+          const uint64_t seen = (hi >= 64 ? ~0ull : hi <= 0 ? 0ull : (1ull << hi) - 1) & (l0 <= 0 ? ~0ull : l0 >= 64 ? 0ull : ~0ull << l0);
+          const uint32_t seen2[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
 #pragma unroll
-            for (int k = 0; k < 64; ++k) s[k >> 5][k & 31] = k < hi ? s[k >> 5][k & 31] : 0xff800000u;
-          }
-          if (j < whole0) {
-#pragma unroll
-            for (int k = 0; k < 64; ++k) s[k >> 5][k & 31] = k >= l0 ? s[k >> 5][k & 31] : 0xff800000u;
-          }
+          for (int k = 0; k < 64; ++k) s[k >> 5][k & 31] = (seen2[k >> 5] & (1u << (k & 31))) ? s[k >> 5][k & 31] : 0xff800000u;
         }
         auto row_max = [&]() -> float {
           float mx[4];
@@ -812,8 +821,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       // ---- epilogue
       const bool any = j1 > j0;
       // (without a key tile: the Q tile has landed)
-      if (!(any ? wait(&bars.o_full[w], (uint32_t)(o_it++ & 1), PA_ERR_O_FULL)
-                : wait(&bars.q_full[n & 1], (uint32_t)((n >> 1) & 1), PA_ERR_Q_FULL)))
+      if (!(any ? wait_out(&bars.o_full[w], (uint32_t)(o_it++ & 1), PA_ERR_O_FULL)
+                : wait_out(&bars.q_full[n & 1], (uint32_t)((n >> 1) & 1), PA_ERR_Q_FULL)))
         break;
       tc_fence_after();
       // The warp's 32 rows go through the item's Q tile, which every S has read, so that the stores are whole
