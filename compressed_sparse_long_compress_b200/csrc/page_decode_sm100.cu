@@ -29,7 +29,7 @@
 // 223 us (6.1 TB/s of codes and scales, 94 % of a copy's rate), 64 of up to 8,192
 // tokens 101 us (81 %): bound by HBM while the CTAs run; the rest is their start,
 // the units' ends and the merge. 16 heads to a key head are bound by the softmax's
-// instructions: 102 us where the bytes take 70.
+// instructions: 95 us where the bytes take 70.
 //
 // CTA roles: warps 0-3 softmax (thread = token, then = dim), warp 4 producer
 // (page table and scales, one tile ahead; TMA of each page's codes, STAGES-deep
@@ -106,6 +106,12 @@ __device__ __forceinline__ void two_parts(float a, float b, uint32_t& hi, uint32
 // 2^d of a whole number d <= 0, 0 below 2^-126 and for NaN.
 __device__ __forceinline__ float pow2i(float d) {
   return __uint_as_float((__float_as_uint(fmaxf(d, -127.f) + 12582912.f) << 23) + 0x3f800000u);
+}
+
+// A softmax warp's mbar_wait, out of line: inlined at each of its waits the code outgrew the instruction
+// cache (16 heads to a key head, pages of 128: 102.8 against 95.1 us; fewer heads: equal).
+__device__ __noinline__ bool pd_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int code) {
+  return mbar_wait(bar, parity, abort, err, code);
 }
 
 struct PdShape {
@@ -444,7 +450,7 @@ __global__ void __launch_bounds__(PD_THREADS, PER) page_decode_sm100_kernel(
     }
     auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
       if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, abortp, errp, code))) w = false;
+      if (!__all_sync(0xffffffffu, pd_wait_slow(bar, parity, abortp, errp, code))) w = false;
     };
     auto load_cols = [&](uint32_t col, float (&x)[N]) {
 #pragma unroll
