@@ -18,9 +18,9 @@
 // a page whose later tokens are larger move its earlier codes to the new
 // scale without a second rounding (but for those that become subnormal).
 // One CTA holds a run in registers between the maximum and the conversion, so
-// the input is read once; HBM bound: 65,536 tokens of 8 heads 73.8 us (5.46 TB/s,
-// 84 % of a copy's rate; the kernel alone 67 us), 13 prompts of up to 2,001 tokens
-// 20.8 us (16.2 us in a captured graph, 93 %).
+// the input is read once; HBM bound: 65,536 tokens of 8 heads 70.1 us (5.74 TB/s,
+// 89 % of a copy's rate), 13 prompts of up to 2,001 tokens 20.8 us (16.2 us in a
+// captured graph, 93 %).
 
 #include "dependent.cuh"
 
@@ -353,14 +353,20 @@ cslc_status launch_page_write(const uint16_t* k, const uint16_t* v, const int32_
                               int n_pages, long long k_stride, long long v_stride, uint8_t* k_cache, uint8_t* v_cache,
                               float* k_scale, float* v_scale, cudaStream_t stream) {
   // A window of a page where that fills the GPU, of fewer tokens where it does not (a step of
-  // 64 single tokens would be one block's). Several heads to a CTA, which then reads the slots
-  // once, while two rounds of CTAs remain: 65,536 tokens 82 -> 74 us, 15,845 tokens 30 -> 28.
+  // 64 single tokens would be one block's).
   int W = page;
   while (W > 1 && (long long)((T + W - 1) / W) * 2 * Hkv < 4 * 148) W >>= 1;
+  // Several heads to a CTA, which then reads the slots once, while CTAs for every SM remain:
+  // pages of 128, 65,536 tokens of 8 heads: 1 / 2 / 4 / 8 heads 82.8 / 75.7 / 73.5 / 70.1 us. The smaller
+  // CTAs of smaller pages want more of them beyond two heads: pages of 64, 40,000 tokens of
+  // 16 heads: 2 / 4 / 8 heads 81.0 / 80.6 / 89.9 us, and 15,845 tokens of 8: 1 / 2 / 4 heads 22.5 / 21.4 / 26.7.
+  const int threads = page < 32 ? 64 : 2 * page, once = 148 * (1024 / threads);   // CTAs that run at a time
   int R = 1;
-  while (R < 8 && (2 * Hkv) % (2 * R) == 0 && (long long)((T + W - 1) / W) * (2 * Hkv / (2 * R)) >= 8 * 148) R *= 2;
+  while (R < 8 && (2 * Hkv) % (2 * R) == 0 &&
+         (long long)((T + W - 1) / W) * (2 * Hkv / (2 * R)) >= (page == PW_MAX_PAGE || R == 1 ? once : once * 5 / 2))
+    R *= 2;
   const unsigned grid = (unsigned)((T + W - 1) / W) * (unsigned)(2 * Hkv / R);
-  const cudaError_t e = launch_after(page_write_kernel, dim3(grid), dim3(page < 32 ? 64 : 2 * page), 0, stream, k, v,
+  const cudaError_t e = launch_after(page_write_kernel, dim3(grid), dim3(threads), 0, stream, k, v,
                                          slots, T, W, R, Hkv, 31 - __builtin_clz(page), n_pages, k_stride, v_stride,
                                          k_cache, v_cache, k_scale, v_scale);
   if (e != cudaSuccess) return set_error(CSLC_ERR_CUDA, "page_write_kernel: %s", cudaGetErrorString(e));
