@@ -405,6 +405,20 @@ def test_decode_window(C, window, P):
     run_decode(C, [3, 200, 777, 130], 8, 2, P, window=window, seed=window)
 
 
+@pytest.mark.parametrize("B,H,Hkv,P,window", [(36, 8, 4, 64, 0), (36, 8, 4, 16, 130), (37, 16, 8, 32, 1), (38, 16, 8, 32, 700),
+                                              (33, 64, 4, 128, 1153), (33, 64, 4, 128, 1154), (3, 40, 1, 64, 300),
+                                              (296, 3, 1, 16, 0), (297, 3, 1, 16, 0)])
+def test_decode_short_units(C, B, H, Hkv, P, window):
+    """Around the sizes where a unit is one CTA's: lengths of 0, 1, the table's and around the window's."""
+    r = np.random.RandomState(B + window)
+    most = 1200 if window == 0 and B < 100 else 3000 if window else 300
+    lens = r.randint(0, most + 1, B)
+    lens[:3] = [0, most, 1]
+    if window and B > 8:
+        lens[3:7] = [window - 1, window, window + 1, window + 127]
+    run_decode(C, [int(n) for n in lens], H, Hkv, P, window=window, seed=B)
+
+
 def test_decode_many_sequences(C):
     r = np.random.RandomState(4)
     run_decode(C, r.randint(0, 90, 400).tolist(), 4, 1, 16, seed=2)
