@@ -720,7 +720,7 @@ cslc_status pd_launch(PdShape sh, const uint16_t* q, const uint8_t* k_cache, con
   const long long units = (long long)sh.B * sh.Hkv * sh.HG;
   const long long tokens = (long long)sh.max_pages << sh.page_log2;
   long long tiles = (tokens + PD_TILE - 1) / PD_TILE;     // of a unit, at most
-  if (sh.window > 0 && sh.window < tokens) tiles = min(tiles, (long long)(sh.window + PD_TILE - 2) / PD_TILE + 1);
+  if (sh.window > 0 && sh.window < tokens) tiles = min(tiles, ((long long)sh.window + PD_TILE - 2) / PD_TILE + 1);
   // Units that are short at any length of their sequences go whole to a CTA each, which saves the
   // merge: 30 sequences of 8 key heads, window 512 / 1,024: 18.7 -> 13.2, 22.6 -> 17.7 us. Where
   // more of them than CTAs run at a time (64 sequences, window 1,024: 37.5 -> 40.7), or few longer ones
