@@ -22,9 +22,9 @@
 // Work. All tiles of all units, in the order of the sequences, are dealt to the
 // CTAs in equal consecutive ranges (two or three CTAs per SM), whatever the lengths are;
 // a unit counts PD_UNIT tiles more for its start and end.
-// (Short units of one turn of CTAs go to a CTA each.)
 // A unit that crosses CTAs leaves fp32 partials in the workspace, which
-// page_decode_combine_kernel (a programmatic dependent launch) merges.
+// page_decode_combine_kernel (a programmatic dependent launch) merges. Short units
+// (small windows, short tables) of one turn of CTAs go to a CTA each, without that.
 //
 // Measured (64 heads on 8, pages of 128 and 64): 8 requests of up to 131,072 tokens
 // 223 us (6.1 TB/s of codes and scales, 94 % of a copy's rate), 64 of up to 8,192
