@@ -73,6 +73,7 @@ constexpr int PA_Q_BYTES = PA_ROWS * 256;        // two halves of 64 dims
 constexpr int PA_KV_BYTES = PA_KEYS * 256;
 constexpr int PA_KV_HALF = PA_KEYS * 128;
 constexpr float PA_SUM_MAX = 65536.f;            // values of up to 2^111 do not overflow O
+constexpr float PA_FAR = 4194304.f;              // 2^22: up to here m log2(e) scale is off by at most 1/4
 constexpr int PA_SMS = 148;
 constexpr int PA_APART = 450;                    // cycles between the Q tiles' softmaxes, in items of more
 constexpr int PA_APART_MIN = 12;                 // key tiles than this
@@ -706,8 +707,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       // tiles masked for no token of the Q tile: [whole0, whole1)
       const int whole0 = sh.window > 0 ? (max(0, tw + it.n[w] - 1 + it.off - sh.window + 1) + PA_KEYS - 1) / PA_KEYS : 0;
       const int whole1 = (tw + it.off + 1) / PA_KEYS;
-      bool far = false;                                  // c m leaves fp32's range for a row of the warp
+      // The reference is M = c m rounded to fp32, the same number wherever it is used. Where that rounding could
+      // move the row's largest probability far from 1 (up to 2^22 by a factor of at most 2^(1/4), from 2^31 on out of
+      // fp32's range) it is c m itself, and c (s - m) is computed from the difference.
+      bool far = false;                                  // such a row is in the warp
       float m = -INFINITY, l = 0.f;
+      auto is_far = [&](float x) { return fabsf(x * c) > PA_FAR; };
       for (int j = j0; j < j1; ++j, ++t_it) {
         const int b = t_it & 1;
         const uint32_t t_p = t_s + 64 + b * 32;
@@ -751,10 +756,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         };
         if (__any_sync(0xffffffffu, m == -INFINITY)) {   // the row's first visible keys set the reference
           if (m == -INFINITY) m = row_max();
-          far = __any_sync(0xffffffffu, fabsf(m * c) > 1e30f && m != -INFINITY);
+          far = __any_sync(0xffffffffu, is_far(m) && m != -INFINITY);
         }
-        // P = 2^(c (s - m)) as bf16, two to a column
-        const float neg = m == -INFINITY ? 0.f : -m * c;
+        // P = 2^(c s - M) as bf16, two to a column
+        const float neg = m == -INFINITY ? 0.f : -__fmul_rn(m, c);
         float2 ps[4];
         uint32_t pk[32];
 #pragma unroll
@@ -768,7 +773,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         }
         ps[0] = add2(add2(ps[0], ps[1]), add2(ps[2], ps[3]));
         float sum = ps[0].x + ps[0].y;
-        // a stale reference (the probabilities leave the range), or c m does: the warp redoes the tile
+        // a stale reference (the probabilities leave the range), or a far one: the warp redoes the tile
         const bool over = !(sum <= PA_SUM_MAX), redo = __any_sync(0xffffffffu, over) || far;
         auto last_pv_done = [&]() -> bool {
           if (j == j0) return true;
@@ -779,16 +784,20 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
         if (redo) {
           if (!last_pv_done()) { ok = false; break; }
           const float mx = over ? fmaxf(row_max(), m) : m;
-          const float alpha = mx > m ? ex2_approx((m - mx) * c) : 1.f;
+          // 2^(old reference - new one); probabilities are 2^((s - base) c + neg2)
+          const bool was_far = is_far(m), now_far = is_far(mx);
+          const float base = now_far && mx != -INFINITY ? mx : 0.f, neg2 = now_far ? 0.f : -__fmul_rn(mx, c);
+          const float up = was_far ? fmaf(m - base, c, neg2) : now_far ? fmaf(-mx, c, __fmul_rn(m, c))
+                                                                      : __fadd_rn(neg2, __fmul_rn(m, c));
+          const float alpha = mx > m ? ex2_approx(up) : 1.f;
           m = mx;
           l *= alpha;
-          far = __any_sync(0xffffffffu, fabsf(m * c) > 1e30f && m != -INFINITY);
+          far = __any_sync(0xffffffffu, now_far && m != -INFINITY);
           if (j > j0) pa_rescale(t_o, alpha);
-          const float ref = m == -INFINITY ? 0.f : m;
           sum = 0.f;
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            const float e0 = ex2_approx((at(2 * k) - ref) * c), e1 = ex2_approx((at(2 * k + 1) - ref) * c);
+            const float e0 = ex2_approx(fmaf(at(2 * k) - base, c, neg2)), e1 = ex2_approx(fmaf(at(2 * k + 1) - base, c, neg2));
             sum += e0 + e1;
             pk[k] = pack_bf16x2(e0, e1);
           }
@@ -832,7 +841,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       pa_stage_rows(t_o, stage, row < rows ? row : -1, any, l == 0.f, inv);
       if (row_ok && lse != nullptr)
         lse[(size_t)(it.q0 + tok) * sh.H + sm->take[n & 1].hk * sh.G + (row - ti * sh.G)] =
-            l == 0.f ? -INFINITY : fmaf(m, sh.scale, log2f(l) * kLn2);
+            l == 0.f ? -INFINITY : fmaf(m, sh.scale, (log2f(l) - (is_far(m) ? 0.f : fmaf(m, c, -__fmul_rn(m, c)))) * kLn2);
       if (any) {
         tc_fence_before();
         __syncwarp();

@@ -58,6 +58,18 @@ def check_attention(got, lse, ref, n, what=""):
     assert (e <= tl).all(), f"{what}: lse off by {e.max():.3e}, allowed {tl[e.argmax()]:.3e}"
 
 
+def check_peaked(got, lse, ref, what):
+    """Rows whose weight is on one key or on equal ones: the roundings of P and of the output are left, and of the
+    lse six to fp32 of numbers of its size (scale, log2(e), their product, the score, the sum, ln(2)), less than 2^-21
+    of it, and what log2 of a few equal ones adds."""
+    o, l, a, _ = ref
+    got, lse = f64(got), f64(lse)
+    err, tol = np.abs(got - o), U * np.abs(o) + (U + 2.0 ** -16) * a
+    assert (err <= tol).all(), f"{what}: {(~(err <= tol)).any(-1).sum()} of {l.size} rows, lse off by {np.abs(lse - l).max():.3e}"
+    tl = 2.0 ** -21 * np.abs(l) + 2.0 ** -16
+    assert (np.abs(lse - l) <= tl).all(), f"{what}: lse off by {np.abs(lse - l).max():.3e}"
+
+
 # ---------------------------------------------------------------- page plan
 
 def run_plan(C, old, new, free, table, page, n_pages, max_tokens):
@@ -346,6 +358,42 @@ def test_prompt_masked_by_the_lowest_value(C):
         ref = PO.attend_rows(f64(q)[t], f64(k)[j, 0], f64(v)[j, 0], 1.0)
         assert (np.abs(got[t] - ref[0]) <= U * np.abs(ref[0]) + (U + 2.0 ** -14) * ref[2]).all()
     assert plain.shape == (63, 2, 128)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("top", [20, 23, 24, 26, 28, 33, 60, 95, 110])
+def test_prompt_large_finite_scores(C, top, sign):
+    """Scores of up to about 2^top whose products are exact, with ties in different tiles: the largest one or the
+    equal largest ones have all the weight, whatever the rounding of a score times log2(e) is."""
+    r = np.random.RandomState(top)
+    T, H, Hkv = 400, 4, 2
+    q, k = torch.zeros(T, H, 128, dtype=BF16, device="cuda"), torch.zeros(T, Hkv, 128, dtype=BF16, device="cuda")
+    v = randn((T, Hkv, 128), top)
+    a = (top + 3) // 2
+    q[:, :, 0] = torch.tensor(sign * 2.0 ** a * (1 + r.randint(0, 128, (T, H)) / 128), dtype=BF16)
+    k[:, :, 0] = torch.tensor(2.0 ** (top + 2 - a - r.randint(0, 3, (T, Hkv))) * (1 + r.randint(0, 8, (T, Hkv)) / 8), dtype=BF16)
+    cu = [0, 270, 400]
+    for window in (0, 90):
+        out, lse = C.prompt_attn(q, k, v, i32(cu), i32(cu), 0.125, window, lse=True)
+        C.sync_status()
+        check_peaked(out, lse, PO.prompt_attention(f64(q), f64(k), f64(v), cu, cu, 0.125, window), f"2^{top}, window {window}")
+
+
+@pytest.mark.parametrize("top", [26, 33, 36, 60, 95])
+def test_prompt_large_finite_scores_alike_in_a_tile(C, top):
+    """As above with one query for all rows of a sequence, so that no other row has a warp compute its scores anew."""
+    r = np.random.RandomState(top)
+    B, n, H = 40, 64, 2
+    q, k = torch.zeros(B * n, H, 128, dtype=BF16, device="cuda"), torch.zeros(B * n, 1, 128, dtype=BF16, device="cuda")
+    v = randn((B * n, 1, 128), top)
+    a = (top + 3) // 2
+    head = np.where(np.arange(B) % 2, -1.0, 1.0) * 2.0 ** a * (1 + r.randint(0, 128, B) / 128)
+    q[:, :, 0] = torch.tensor(np.repeat(head, n)[:, None], dtype=BF16)
+    k[:, 0, 0] = torch.tensor(2.0 ** (top + 2 - a) * (1 + r.randint(0, 8, B * n) / 8), dtype=BF16)
+    cu = list(range(0, B * n + 1, n))
+    out, lse = C.prompt_attn(q, k, v, i32(cu), i32(cu), 0.125, lse=True)
+    C.sync_status()
+    check_peaked(out, lse, PO.prompt_attention(f64(q), f64(k), f64(v), cu, cu, 0.125), f"2^{top}")
 
 
 def test_prompt_long_rows_sampled(C):
