@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
     __syncwarp();
   } else if (warp >= PA_MMA_WARP) {
     // ------------------------------------------------- MMA issuer of Q tile w
-    // The whole warp walks the loop and one elected lane issues: descriptors stay
+    // The whole warp walks the loop and one elected lane (always the same) waits and issues: descriptors stay
     // in uniform registers (a lone thread took 77-88 cycles for a product of 64).
     constexpr uint32_t ID_S = idesc_bf16(PA_ROWS, PA_KEYS, false, false);
     constexpr uint32_t ID_O = idesc_bf16(PA_ROWS, 128, false, true);
@@ -573,15 +573,18 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
     const uint32_t t_s = uni(tmem + w * 128), t_o = uni(tmem + 256 + w * 128);
     int slot = 0, ph = 0;                                // the ring, in the order of use
     int s_it = 0, p_it = 0, o_it = 0, slow_it = 0;       // S and P tiles, items with a tile, tiles not done here
+    // A lane's own, as giving up a wait is: around an abort one lane may see a phase complete and another the flag
+    // or the limit. Such a lane issues nothing more but walks on with the others, through elections and shuffles, and
+    // the warp leaves by the vote at the next item. (A vote behind each wait of the whole warp: 8,192 tokens
+    // 1.00 -> 1.10 ms; waits of one lane: equal.)
     bool ok = true;
-    // the slot's products are issued (or it is the other Q tile's alone): release it
-    auto release = [&]() {
-      if (elect_one()) mma_commit(&bars.empty[slot]);
-      __syncwarp();
-      if (++slot == PA_SLOTS) { slot = 0; ph ^= 1; }
+    auto wait = [&](uint64_t* bar, int parity, int code) {
+      ok = ok && mbar_wait(bar, (uint32_t)(parity & 1), abortp, errp, code);
     };
-    for (int n = 0; ok; ++n) {
-      if (!mbar_wait(&bars.item_full[n & 1], (uint32_t)((n >> 1) & 1), abortp, errp, PA_ERR_ITEM)) break;
+    auto next_slot = [&]() { if (++slot == PA_SLOTS) { slot = 0; ph ^= 1; } };
+    for (int n = 0;; ++n) {
+      wait(&bars.item_full[n & 1], n >> 1, PA_ERR_ITEM);
+      if (!__all_sync(0xffffffffu, ok)) break;
       const PaTake t = sm->take[n & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.item_empty[n & 1]);
@@ -590,70 +593,64 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
       const uint32_t q0 = uni(smem_u32(q_s + ((n & 1) * 2 + w) * PA_Q_BYTES) >> 4);
       const int js = uni(w == 0 ? it.s[0] : it.s[1]), je = uni(w == 0 ? it.e[0] : it.e[1]);
       const int jb = uni(it.jb), jend = uni(it.je);
-      if (!mbar_wait(&bars.q_full[n & 1], (uint32_t)((n >> 1) & 1), abortp, errp, PA_ERR_Q_FULL)) break;
-      auto issue_s = [&](int j) {
-        ok = ok && mbar_wait(&bars.full[slot], (uint32_t)ph, abortp, errp, PA_ERR_K_FULL);
-        if (ok && j >= js && j < je && s_it > 0)         // the last scores are in registers
-          ok = mbar_wait(&bars.s_read[w], (uint32_t)((s_it - 1) & 1), abortp, errp, PA_ERR_S_READ);
-        if (!ok) return;
-        if (j >= js && j < je) {
-          tc_fence_after();
-          const uint32_t lb = uni(r0 + slot * (PA_KV_BYTES / 16));
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_bf16(t_s, d_kmaj | (q0 + ((k >> 2) * (PA_ROWS * 128) + (k & 3) * 32) / 16),
-                       d_kmaj | (lb + ((k >> 2) * PA_KV_HALF + (k & 3) * 32) / 16), ID_S, k > 0 ? 1u : 0u);
-            mma_commit(&bars.s_full[w]);
-          }
-          __syncwarp();
-          ++s_it;
-        }
-        release();
-        if (j == jend - 1) {                             // every S of the item has read Q
-          if (elect_one()) mma_commit(&bars.q_empty[n & 1]);
-          __syncwarp();
-        }
-      };
+      wait(&bars.q_full[n & 1], n >> 1, PA_ERR_Q_FULL);
       if (jb == jend) {
-        if (elect_one()) mma_commit(&bars.q_empty[n & 1]);
+        if (elect_one() && ok) mma_commit(&bars.q_empty[n & 1]);
         __syncwarp();
       }
-      if (jb < jend) issue_s(jb);
-      for (int j = jb; j < jend && ok; ++j) {
-        if (j + 1 < jend) issue_s(j + 1);
-        ok = ok && mbar_wait(&bars.full[slot], (uint32_t)ph, abortp, errp, PA_ERR_V_FULL);
-        if (j >= js && j < je) {
-          const bool first = j == js;
-          const int b = p_it & 1;
-          if (first && o_it > 0)
-            ok = ok && mbar_wait(&bars.o_free[w], (uint32_t)((o_it - 1) & 1), abortp, errp, PA_ERR_O_FREE);
-          if (first) ++o_it;
-          const uint32_t lo = uni(r0 + slot * (PA_KV_BYTES / 16)), a = uni(t_s + 64 + b * 32);
-          ok = ok && mbar_wait(&bars.p_full[w][b], (uint32_t)((p_it >> 1) & 1), abortp, errp, PA_ERR_P_FULL);
-          if (!ok) break;
-          ++p_it;
-          tc_fence_after();
-          // a V tile that is not finite where some row does not see it: the softmax warps did the product
-          const bool mine = reinterpret_cast<volatile int*>(sm->bad_v[w])[b] != p_it;
-          if (!mine) {
-            ok = mbar_wait(&bars.slow_done[w], (uint32_t)(slow_it++ & 1), abortp, errp, PA_ERR_SLOW);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          if (elect_one()) {
-            if (mine) {
+      auto issue_s = [&](int j) {
+        const bool use = j >= js && j < je;
+        const uint32_t lb = uni(r0 + slot * (PA_KV_BYTES / 16));
+        if (elect_one()) {
+          wait(&bars.full[slot], ph, PA_ERR_K_FULL);
+          if (use && s_it > 0) wait(&bars.s_read[w], s_it - 1, PA_ERR_S_READ);   // the last scores are in registers
+          if (ok) {
+            if (use) {
+              tc_fence_after();
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_bf16_ts(t_o, a + k * 8, d_mnmaj | (lo + k * (2048 / 16)), ID_O, (!first || k > 0) ? 1u : 0u);
+              for (int k = 0; k < 8; ++k)
+                mma_bf16(t_s, d_kmaj | (q0 + ((k >> 2) * (PA_ROWS * 128) + (k & 3) * 32) / 16),
+                         d_kmaj | (lb + ((k >> 2) * PA_KV_HALF + (k & 3) * 32) / 16), ID_S, k > 0 ? 1u : 0u);
+              mma_commit(&bars.s_full[w]);
             }
-            mma_commit(&bars.pv_done[w][b]);
-            if (j == je - 1) mma_commit(&bars.o_full[w]);
+            mma_commit(&bars.empty[slot]);               // (or it is the other Q tile's alone)
+            if (j == jend - 1) mma_commit(&bars.q_empty[n & 1]);   // every S of the item has read Q
           }
-          __syncwarp();
         }
-        if (!ok) break;
-        release();
+        __syncwarp();
+        if (use) ++s_it;
+        next_slot();
+      };
+      if (jb < jend) issue_s(jb);
+      for (int j = jb; j < jend; ++j) {
+        if (j + 1 < jend) issue_s(j + 1);
+        const bool use = j >= js && j < je, first = j == js;
+        const int b = p_it & 1;
+        const uint32_t lo = uni(r0 + slot * (PA_KV_BYTES / 16)), a = uni(t_s + 64 + b * 32);
+        if (elect_one()) {
+          wait(&bars.full[slot], ph, PA_ERR_V_FULL);
+          if (use) {
+            if (first && o_it > 0) wait(&bars.o_free[w], o_it - 1, PA_ERR_O_FREE);
+            wait(&bars.p_full[w][b], p_it >> 1, PA_ERR_P_FULL);
+            // a V tile that is not finite where some row does not see it: the softmax warps did the product
+            const bool mine = reinterpret_cast<volatile int*>(sm->bad_v[w])[b] != p_it + 1;
+            if (!mine) wait(&bars.slow_done[w], slow_it++, PA_ERR_SLOW);
+            if (ok) {
+              tc_fence_after();
+              if (mine) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_bf16_ts(t_o, a + k * 8, d_mnmaj | (lo + k * (2048 / 16)), ID_O, (!first || k > 0) ? 1u : 0u);
+              }
+              mma_commit(&bars.pv_done[w][b]);
+              if (j == je - 1) mma_commit(&bars.o_full[w]);
+            }
+          }
+          if (ok) mma_commit(&bars.empty[slot]);
+        }
+        __syncwarp();
+        if (use) { ++p_it; if (first) ++o_it; }
+        next_slot();
       }
     }
     if (elect_one()) mma_commit(&bars.final_bar[w]);

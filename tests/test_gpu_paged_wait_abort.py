@@ -60,3 +60,26 @@ def test_prompt_wait_abort_then_recovers(C):
     C.sync_status()
     ref = PO.prompt_attention(TP.f64(q), TP.f64(k), TP.f64(v), cu, cu, TP.SCALE, rows={0, 5, 1699, 1700, 1701, 2999})
     TP.check_attention(out, lse, ref, 1700, "prompt after an abort")
+
+
+@pytest.mark.parametrize("limit_ns", [0, 100, 400, 1500, 6000, 25000])
+def test_prompt_waits_that_run_out_at_any_time(C, limit_ns):
+    """Limits in the range of the kernel's own waits: some run out, in any role, each call ends, and the next ones
+    with the usual limit have the bits of before."""
+    q, k, v = TP.randn((4000, 8, 128), 1), TP.randn((4000, 2, 128), 2), TP.randn((4000, 2, 128), 3)
+    v[::300, 1] = math.nan                                    # products on the CUDA cores, too
+    cu = TP.i32([0, 1700, 1810, 1811, 3000, 4000])
+    want = C.prompt_attn(q, k, v, cu, cu, TP.SCALE, 500, lse=True)
+    C.sync_status()
+    C.testing_set_wait_limits(limit_ns, 0)
+    for _ in range(10):
+        C.prompt_attn(q, k, v, cu, cu, TP.SCALE, 500, lse=True)
+        try:
+            C.sync_status()
+        except C.CslcError as e:
+            assert e.status == 7 and "cslc_prompt_attn" in str(e)
+    C.testing_set_wait_limits(C.WAIT_LIMIT_NS_DEFAULT, C.WAIT_SLEEP_NS_DEFAULT)
+    got = C.prompt_attn(q, k, v, cu, cu, TP.SCALE, 500, lse=True)
+    C.sync_status()
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))

@@ -3,6 +3,8 @@
 
 import ctypes
 import math
+import os
+import re
 
 import numpy as np
 import pytest
@@ -213,3 +215,26 @@ def test_binding_refuses_what_it_cannot_pass_on():
         cslc.prompt_attn(q, q[:, :2], q[:, :2], cu, cu, 0.1)
     with pytest.raises(TypeError, match="bfloat16"):
         cslc.prompt_attn(q.float(), q[:, :2], q[:, :2], cu, cu, 0.1)
+
+
+def test_lanes_of_a_warp_leave_together():
+    """In the prompt kernel a wait gives up by each lane's own clock. Warps that go on to collective instructions
+    (elections, shuffles) take one decision for all lanes; the producer is a single lane."""
+    text = open(os.path.join(os.path.dirname(cslc.__file__), "csrc", "prompt_attn_sm100.cu")).read()
+    text = text[text.index("prompt_attn_sm100_kernel("):text.index("size_t prompt_attn_workspace_bytes")]
+    text = re.sub(r"//[^\n]*", "", text)
+    at = [text.index(x) for x in ("if (warp == PA_PROD_WARP)", "else if (warp >= PA_MMA_WARP)", "const int row = tid & 127")]
+    producer, issue, softmax = text[at[0]:at[1]], text[at[1]:at[2]], text[at[2]:]
+    assert producer.index("if (lane == 0) {") < producer.index("pa_wait(") and text.count("pa_wait(") == producer.count("pa_wait(")
+    voted = re.findall(r"(\S+ )(?:mbar_wait|pa_wait_slow)\(", softmax)
+    assert voted and set(voted) <= {"__all_sync(0xffffffffu, ", "return ", "0xffffffffu, "} and "return mbar" not in softmax
+    # the issuing warps: what a lane's wait says stays its own, and no collective is reached by some lanes only
+    assert len(re.findall(r"mbar_wait\(", issue)) == 1 and "ok = ok && mbar_wait(" in issue
+    leave = re.findall(r"[^\n]*\b(?:break|return);", issue)
+    assert leave and all("!__all_sync(0xffffffffu, ok)" in x or "!t.there" in x for x in leave), leave
+    elected = re.findall(r"if \(elect_one\(\)\) \{.*?\n +__syncwarp\(\);", issue, re.S)
+    assert len(elected) == 2
+    for block in elected:
+        assert not re.search(r"uni\(|__shfl|__all|__any|elect_one", block[len("if (elect_one())"):])
+        issue = issue.replace(block, "")
+    assert re.findall(r"\bwait\(&bars\.(\w+)", issue) == ["item_full", "q_full"]
