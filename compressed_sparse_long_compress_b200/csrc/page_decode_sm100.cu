@@ -534,8 +534,10 @@ __global__ void __launch_bounds__(PD_THREADS, PER) page_decode_sm100_kernel(
           float mx = (&sm->smax[sb][8 * k][0])[lane];     // 8 heads x 4 warps
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          // the tile's largest probability becomes 2^7 .. 2^8; no score at all leaves -inf
-          const float r = ceilf(mx) - 8.f, Rn = fmaxf(R[k], r);
+          // the tile's largest probability becomes 2^7 .. 2^8; no score at all leaves -inf. From 2^27 on the step of
+          // fp32's is above 8 (a reference 16 below would make it 2^16, and e4m3 saturates): it becomes 1, and what is a
+          // step or more below it, 2^-16, is lost: 127 of those are 2^-9 of the sum.
+          const float r = ceilf(mx) - (fabsf(mx) < 134217728.f ? 8.f : 0.f), Rn = fmaxf(R[k], r);
           up = up || r > R[k];
           fl[k] = pow2i(r - Rn);
           al[k] = pow2i(R[k] - Rn);

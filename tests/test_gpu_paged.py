@@ -481,6 +481,31 @@ def test_decode_flat_and_peaked(C, q_std):
     run_decode(C, [900, 40], 8, 2, 32, seed=6, q_std=q_std)
 
 
+@pytest.mark.parametrize("H,P", [(8, 16), (8, 64), (16, 64)])
+@pytest.mark.parametrize("top", [24, 26, 27, 28, 29, 33, 60, 95])
+def test_decode_large_finite_scores(C, top, H, P):
+    """Base-2 scores around +-2^top (from 2^27 on 8 is no whole step of fp32's): equal largest ones share all the weight."""
+    r = np.random.RandomState(top + H)
+    lens = [700, 40, 1, 3000] * 3
+    pages = [-(-n // P) for n in lens]
+    kc, vc, ks, vs = make_cache(sum(pages), 1, P, top)
+    vs[:] = 2.0 ** -7
+    ks[:] = 2.0 ** -7
+    levels = torch.tensor([1, 1.125, 1.25, 1.5, 2], device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+    kc[:, 0, :, 0] = levels[torch.tensor(r.randint(0, 5, (sum(pages), P)), device="cuda")]
+    table, at = np.zeros((len(lens), max(pages)), dtype=np.int64), 0
+    for b, m in enumerate(pages):
+        table[b, :m] = at + r.permutation(m)
+        at += m
+    q = torch.zeros(len(lens), H, 128, dtype=BF16, device="cuda")
+    sign = np.where(np.arange(H) % 2, -1.0, 1.0)
+    q[:, :, 0] = torch.tensor(sign * 2.0 ** (top + 7 + 2) * (1 + r.randint(0, 128, (len(lens), H)) / 128), dtype=BF16)
+    out, lse = C.page_decode_attn(q, kc, vc, ks, vs, i32(table), i32(lens), 0.125, lse=True)
+    C.sync_status()
+    ref = PO.page_decode_attention(f64(q), kc.cpu().numpy(), vc.cpu().numpy(), f64(ks), f64(vs), table, lens, 0.125)
+    check_peaked(out, lse, ref, f"2^{top}")
+
+
 def test_decode_scales_far_apart(C):
     """Pages whose scales differ by up to 2^30: neither values nor weights get lost."""
     run_decode(C, [700, 129], 8, 2, 16, seed=8, spread=30)
