@@ -91,6 +91,14 @@ static bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
     REQUIRE(aligned16(p), CSLC_ERR_ALIGN, "%s: %s is not 16-byte aligned", __func__, #p); \
   } while (0)
 
+// int32 lists that are only read, an element at a time: slices of longer lists.
+#define REQUIRE_LIST(p)                                                                \
+  do {                                                                                 \
+    REQUIRE((p) != nullptr, CSLC_ERR_NULL, "%s: %s is NULL", __func__, #p);            \
+    REQUIRE(reinterpret_cast<uintptr_t>(p) % sizeof(int32_t) == 0, CSLC_ERR_ALIGN, "%s: %s is not 4-byte aligned", \
+            __func__, #p);                                                             \
+  } while (0)
+
 // When the caller does not keep the scores they are produced in blocks of
 // this many rows (up to 4 GiB of scores), two blocks in flight when there are
 // more: the top-k of one block runs on an auxiliary stream beside the indexer
@@ -565,10 +573,10 @@ cslc_status cslc_page_plan(const int32_t* old_len, const int32_t* new_len, int B
   FORWARD(check_pages("cslc_page_plan", 1, page, n_pages));
   REQUIRE_PTR(cu); REQUIRE_PTR(status);
   if (B > 0) {
-    REQUIRE_PTR(old_len); REQUIRE_PTR(new_len); REQUIRE_PTR(seq_len);
+    REQUIRE_LIST(old_len); REQUIRE_LIST(new_len); REQUIRE_PTR(seq_len);
     if (max_pages > 0) REQUIRE_PTR(block_table);
   }
-  if (n_free > 0) REQUIRE_PTR(free_pages);
+  if (n_free > 0) REQUIRE_LIST(free_pages);
   if (max_tokens > 0) REQUIRE_PTR(slots);
   // other CTAs still read the inputs when one writes its results
   const size_t w = sizeof(int32_t);
@@ -593,7 +601,7 @@ cslc_status cslc_page_write_e4m3(const cslc_bf16* k, const cslc_bf16* v, const i
   FORWARD(check_stride(fn, "v_stride", v_stride, Hkv));
   REQUIRE((long long)T * 2 * Hkv < (1ll << 31), CSLC_ERR_UNSUPPORTED, "%s: T * 2 * H_kv must be below 2^31", fn);
   if (T == 0 || n_pages == 0) return CSLC_OK;
-  REQUIRE_PTR(k); REQUIRE_PTR(v); REQUIRE_PTR(slots);
+  REQUIRE_PTR(k); REQUIRE_PTR(v); REQUIRE_LIST(slots);
   REQUIRE_PTR(k_cache); REQUIRE_PTR(v_cache); REQUIRE_PTR(k_scale); REQUIRE_PTR(v_scale);
   return launch_page_write(k, v, slots, T, Hkv, page, n_pages, k_stride, v_stride, k_cache, v_cache, k_scale, v_scale,
                            stream);
@@ -619,7 +627,7 @@ cslc_status cslc_prompt_attn(const cslc_bf16* q, const cslc_bf16* k, const cslc_
   REQUIRE((long long)Tq * H < (1ll << 31) && (long long)Tk * Hkv < (1ll << 31), CSLC_ERR_UNSUPPORTED,
           "%s: Tq * H and Tk * H_kv must be below 2^31", fn);
   if (B == 0 || Tq == 0) return CSLC_OK;
-  REQUIRE_PTR(q); REQUIRE_PTR(cu_q); REQUIRE_PTR(cu_k); REQUIRE_PTR(out);
+  REQUIRE_PTR(q); REQUIRE_LIST(cu_q); REQUIRE_LIST(cu_k); REQUIRE_PTR(out);
   if (Tk > 0) { REQUIRE_PTR(k); REQUIRE_PTR(v); }
   if (lse) REQUIRE_PTR(lse);
   const size_t need = prompt_attn_workspace_bytes(B, Tq, H, Hkv);

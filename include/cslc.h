@@ -24,7 +24,8 @@
  *   - Tensors are dense, row-major (last index fastest) with the shapes given
  *     below; the paged entry points take a row stride for some. bf16 tensors
  *     are passed as cslc_bf16 (raw bfloat16 bits).
- *     Every pointer must be 16-byte aligned (CSLC_ERR_ALIGN otherwise).
+ *     Every pointer must be 16-byte aligned (CSLC_ERR_ALIGN otherwise), but
+ *     for a few lists of the paged entry points.
  *   - Calls are asynchronous on `stream` (NULL = the legacy default stream) and
  *     return after the launches are enqueued. Arguments are validated before
  *     anything is launched: on any error status nothing has been written.
@@ -381,6 +382,9 @@ cslc_status cslc_decode_topk(const float* scores, const int32_t* n_entries, int 
  *
  * Query head h reads key / value head h / (H / H_kv): H is a multiple of H_kv,
  * 1 <= H <= 128. D must be 128.
+ *
+ * The lists old_len, new_len, free_pages, cu_q and cu_k, and slots where it is
+ * read, may be slices of longer ones: 4-byte alignment is enough for them.
  */
 
 /* Page plan: for requests that hold old_len[b] tokens and get new_len[b] more

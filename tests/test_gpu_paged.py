@@ -856,3 +856,37 @@ def test_binding_refusals_on_the_device(C):
                            i32([1] * 4), SCALE)
     with pytest.raises(ValueError, match="max_tokens"):
         C.page_plan(cu, cu, cu, i32(np.zeros((2, 2))), 16, 4)
+
+
+def test_plans_one_after_another_from_what_is_left(C):
+    """The caller takes status[0] pages off the front of its list, whatever their number; other lists as slices, too."""
+    page, n_pages, lists = 16, 40, i32([9] + [20, 0, 5, 3, 9] + [7])
+    pool = np.random.RandomState(3).permutation(n_pages)
+    free, at = i32(pool), 0
+    for new, taken in (([3, 16, 0, 13, 0], 1), ([13, 0, 12, 0, 0], 2), ([29, 0, 12, 0, 0], 3), ([1, 1, 1, 1, 1], 1), ([30] * 5, 10)):
+        old = lists[1:6]
+        table = np.full((5, 9), -1)
+        for b, m in enumerate((2, 0, 1, 1, 1)):
+            table[b, :m] = 30 + b
+        got = C.page_plan(old, i32([0] + new)[1:], free[at:], i32(table), page, n_pages, max_tokens=200)
+        ref = PO.page_plan(old.tolist(), new, pool[at:], table, page, n_pages, 200)
+        for g, r in zip(got, ref[1:]):
+            assert np.array_equal(g.cpu().numpy(), r)
+        assert int(got[3][0]) == taken
+        at += taken
+
+
+def test_lists_that_are_slices(C):
+    q, k, v = randn((90, 4, 128), 1), randn((90, 2, 128), 2), randn((90, 2, 128), 3)
+    cu = i32([0, 3, 4, 50, 90])
+    for i in (1, 2, 3):
+        out, lse = torch.full_like(q, 7.0), torch.full((90, 4), 9.0, device="cuda")
+        C.prompt_attn(q, k, v, cu[i:], cu[i:], SCALE, out=out, lse=lse)
+        C.sync_status()
+        c = cu.tolist()[i:]
+        check_attention(out, lse, PO.prompt_attention(f64(q), f64(k), f64(v), c, c, SCALE), 50)
+        assert (f64(out)[:c[0]] == 7).all() and (f64(lse)[:c[0]] == 9).all()
+    kc, ks = empty_cache(6, 2, 16)
+    vc, vs = empty_cache(6, 2, 16)
+    slots = i32(range(17, 17 + 70))
+    run_write(C, k[:61], v[:61], slots[3:64], kc, vc, ks, vs)

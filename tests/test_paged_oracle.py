@@ -238,3 +238,23 @@ def test_lanes_of_a_warp_leave_together():
         assert not re.search(r"uni\(|__shfl|__all|__any|elect_one", block[len("if (elect_one())"):])
         issue = issue.replace(block, "")
     assert re.findall(r"\bwait\(&bars\.(\w+)", issue) == ["item_full", "q_full"]
+
+
+def test_lists_may_be_slices():
+    """4-byte alignment of what is only read element by element (shown by the next check's refusal), 16 of the rest."""
+    four, two = 0x1004, 0x1002
+    for name in ("old", "new", "free"):
+        st, msg = _plan(**{name: two})
+        assert st == 3 and "4-byte" in msg, name
+        st, msg = _plan(**{name: four, "cu": four})               # the result is not aligned
+        assert st == 3 and "cu is not 16-byte" in msg, name
+        at = {"old": 1 << 30, "new": 1 << 31, "free": 1 << 32, "table": 5 << 30, "slots": 6 << 30, "seq": 7 << 30, "cu": 8 << 30}
+        st, msg = _plan(**{**at, name: at[name] + 4, "status": at[name]})
+        assert st == 4 and "overlaps" in msg, name
+    assert _write(slots=two)[0] == 3 and "4-byte" in _write(slots=two)[1]
+    st, msg = _write(slots=four, kc=ODD)
+    assert st == 3 and "k_cache" in msg
+    for name in ("cq", "ck"):
+        assert _prompt(**{name: two})[0] == 3
+        st, msg = _prompt(**{name: four}, q=1 << 30, out=1 << 30)
+        assert st == 4 and "overlaps" in msg, name
