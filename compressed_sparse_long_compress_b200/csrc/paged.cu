@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(PP_THREADS) page_plan_kernel(
   int32_t* tok = pp_smem;              // [B + 1] tokens before sequence b
   int32_t* pg = tok + B + 1;           // [B + 1] pages handed out before sequence b
   __shared__ long long wsum[PP_THREADS / 32][2];
-  __shared__ int lost_s;
+  __shared__ unsigned long long lost_s;   // lengths of any int32 value: more than 32 bits hold
   const int tid = threadIdx.x;
   const int P = 1 << page_log2;
   const int per = (B + PP_THREADS - 1) / PP_THREADS;
@@ -147,12 +147,12 @@ __global__ void __launch_bounds__(PP_THREADS) page_plan_kernel(
       const long long o = max(old_len[b], 0), end = o + max(new_len[b], 0);
       lost += min(end, x0 + P) - x0;
     }
-  if (lost) atomicAdd(&lost_s, sat32(lost));
+  if (lost) atomicAdd(&lost_s, (unsigned long long)lost);
   __syncthreads();
   if (tid == 0) {
     cu[B] = T;
     status[0] = taken;
-    status[1] = lost_s;
+    status[1] = sat32((long long)lost_s);
   }
 }
 

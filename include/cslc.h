@@ -405,6 +405,7 @@ cslc_status cslc_decode_topk(const float* scores, const int32_t* n_entries, int 
  *   seq_len [B] int32: old_len + new_len
  *   status [2] int32: pages handed out (more than n_free when the list was too
  *       short), and new tokens that have no page (0 when all went well)
+ * Sums that int32 cannot hold read 2^31 - 1.
  * 0 <= B <= 8192. The caller takes the first status[0] pages off its list.
  * No result may overlap old_len, new_len or free_pages. One launch; no workspace. */
 cslc_status cslc_page_plan(const int32_t* old_len, const int32_t* new_len, int B, const int32_t* free_pages,

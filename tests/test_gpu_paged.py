@@ -145,6 +145,15 @@ def test_plan_large_lengths(C):
     assert run[1].tolist() == [0, 0, 3, 3] and run[2].tolist() == [big, 3, 5]
 
 
+def test_plan_counts_more_lost_tokens_than_32_bits_hold(C):
+    table = i32(np.full((4, 2), -1))
+    for n, lost in (([2 ** 30] * 4, 2 ** 31 - 1), ([2 ** 30, 2 ** 30, 0, 0], 2 ** 31 - 1), ([2 ** 30, 2 ** 30 - 1, 0, 0], 2 ** 31 - 1),
+                    ([2 ** 30, 5, 0, 0], 2 ** 30 + 5)):
+        slots, cu, total, st = C.page_plan(i32([0] * 4), i32(n), i32([]), table.clone(), 16, 8, max_tokens=3)
+        assert st.tolist()[1] == lost and slots.tolist() == [-1] * 3
+        assert cu.tolist() == [min(sum(n[:i]), 2 ** 31 - 1) for i in range(5)] and total.tolist() == n
+
+
 # -------------------------------------------------------------- cache write
 
 def empty_cache(n_pages, Hkv, P, fill=0):
