@@ -250,8 +250,8 @@ __device__ __noinline__ void pa_rescale(uint32_t t_o, float alpha) {
     tmem_st32(t_o + k * 32, r);
   }
 }
-// O += P V on the CUDA cores, entries with P = 0 left out; the products into O are done.
-__device__ __noinline__ void pa_slow_pv(uint32_t t_o, uint32_t t_p, const uint8_t* v_s, bool first) {
+// O += P V on the CUDA cores over the keys k0 .. k1 - 1 of the tile, which the row sees; the products into O are done.
+__device__ __noinline__ void pa_slow_pv(uint32_t t_o, uint32_t t_p, const uint8_t* v_s, int k0, int k1, bool first) {
 #pragma unroll 1
   for (int k = 0; k < 4; ++k) {                          // 32 dims at a time
     uint32_t r[32];
@@ -275,7 +275,7 @@ __device__ __noinline__ void pa_slow_pv(uint32_t t_o, uint32_t t_p, const uint8_
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int d = q * 8 + 2 * i;
-          if (p != 0.f) {
+          if (key >= k0 && key < k1) {
             r[d] = __float_as_uint(fmaf(p, bf16_lo(u4[i]), __uint_as_float(r[d])));
             r[d + 1] = __float_as_uint(fmaf(p, bf16_hi(u4[i]), __uint_as_float(r[d + 1])));
           }
@@ -815,7 +815,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1) prompt_attn_sm100_kernel(
           if (!wait(&bars.p_full[w][b], (uint32_t)((t_it >> 1) & 1), PA_ERR_P_FULL)) { ok = false; break; }
           if (reinterpret_cast<volatile int*>(sm->bad_v[w])[b] == t_it + 1) {
             if (!last_pv_done()) { ok = false; break; }
-            pa_slow_pv(t_o, t_p, ring + (vv() % PA_SLOTS) * PA_KV_BYTES, j == j0);
+            pa_slow_pv(t_o, t_p, ring + (vv() % PA_SLOTS) * PA_KV_BYTES, lo - j * PA_KEYS, last + 1 - j * PA_KEYS, j == j0);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.slow_done[w]);

@@ -337,6 +337,23 @@ def test_prompt_what_is_not_seen_has_no_influence(C):
         assert np.isnan(got[sees(100)][:, :, ::7]).any(axis=2).all()       # rows that do see them
 
 
+def test_prompt_nan_value_of_no_weight_that_is_seen(C):
+    """A NaN that a row sees stays NaN where its probability is 0 in fp32, in whole tiles and in those that are masked in part."""
+    T = 200
+    q, k, v = (torch.zeros(T, 1, 128, dtype=BF16, device="cuda") for _ in range(3))
+    q[:, 0, 0], k[:, 0, 0] = 1.0, 1.0
+    v[:] = 1.0
+    for at in (3, 70, 130):
+        k[at, 0, 0] = -1000.0
+        v[at, 0, at % 7] = math.nan
+    out, lse = C.prompt_attn(q, k, v, i32([0, T]), i32([0, T]), 1.0, lse=True)
+    C.sync_status()
+    o, sees = f64(out)[:, 0], np.zeros((T, 128), dtype=bool)
+    for at in (3, 70, 130):
+        sees[at:, at % 7] = True
+    assert np.array_equal(np.isnan(o), sees) and np.isfinite(f64(lse)).all()
+
+
 def test_prompt_infinite_value_is_infinite_where_it_is_seen(C):
     q, k, v = randn((200, 2, 128), 1), randn((200, 1, 128), 2), randn((200, 1, 128), 3)
     v[130, 0, 5], v[131, 0, 9] = math.inf, -math.inf
