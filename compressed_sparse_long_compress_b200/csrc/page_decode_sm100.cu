@@ -275,9 +275,9 @@ __global__ void __launch_bounds__(PD_THREADS, PER) page_decode_sm100_kernel(
     const int P = 1 << sh.page_log2;
     if (lane == 0) { tma_prefetch_map(&tm_k); tma_prefetch_map(&tm_v); }
     int it = 0;
-    // lane i < ppt holds page i of the tile
-    auto load = [&](int b, int u, int lo, int n, int tile, int& y, float& ks, int& ev) {
-      y = -1; ks = 0.f; ev = PD_ABSENT;
+    // lane i < ppt holds page i of the tile: its first row (-1: there is none), its scales
+    auto load = [&](int b, int u, int lo, int n, int tile, int& y, float& ks, float& vs) {
+      y = -1; ks = vs = 0.f;
       if (lane < ppt) {
         const long long j = (long long)tile * ppt + lane;
         const long long tok = j << sh.page_log2;
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(PD_THREADS, PER) page_decode_sm100_kernel(
             const size_t ps = (size_t)pid * sh.Hkv + hk;
             y = (int)(ps << sh.page_log2);
             ks = k_scale[ps];
-            ev = min(max((int)((__float_as_uint(v_scale[ps]) >> 23) & 0xff) - 127, -40), 60);
+            vs = v_scale[ps];
           }
         }
       }
@@ -353,24 +353,27 @@ __global__ void __launch_bounds__(PD_THREADS, PER) page_decode_sm100_kernel(
       ++seg;
       return true;
     };
-    int y = -1, ev = PD_ABSENT;
-    float ks = 0.f;
+    int y = -1;
+    float ks = 0.f, vs = 0.f;
     bool more = advance();
-    if (more) load(walk.b, walk.u, lo, n, t0 + walk.t, y, ks, ev);
+    if (more) load(walk.b, walk.u, lo, n, t0 + walk.t, y, ks, vs);
     while (more) {
       const int s = it % STAGES;
       const bool new_seg = i == 0;
       const int seg_now = seg, b_now = walk.b, u_now = walk.u;
-      int y2 = -1, ev2 = PD_ABSENT;
-      float ks2 = 0.f;
+      int y2 = -1;
+      float ks2 = 0.f, vs2 = 0.f;
       more = advance();
-      if (more) load(walk.b, walk.u, lo, n, t0 + walk.t + i, y2, ks2, ev2);
+      if (more) load(walk.b, walk.u, lo, n, t0 + walk.t + i, y2, ks2, vs2);
       if (it >= STAGES) {
         bool w = true;
         if (lane == 0) w = mbar_wait(&bars.empty[s], (uint32_t)((it / STAGES - 1) & 1), abortp, errp, PD_ERR_EMPTY);
         if (!__shfl_sync(0xffffffffu, (int)w, 0)) break;
       }
-      if (lane < ppt) { sm->ks[s][lane] = ks; sm->ev[s][lane] = ev; }
+      if (lane < ppt) {
+        sm->ks[s][lane] = y >= 0 ? pow2(page_scale_exponent(ks)) : 0.f;
+        sm->ev[s][lane] = y >= 0 ? page_scale_exponent(vs) : PD_ABSENT;
+      }
       __syncwarp();
       if (lane == 0) { mbar_arrive_expect_tx(&bars.k_full[s], PD_HALF); mbar_arrive_expect_tx(&bars.v_full[s], PD_HALF); }
       __syncwarp();
@@ -383,7 +386,7 @@ __global__ void __launch_bounds__(PD_THREADS, PER) page_decode_sm100_kernel(
       }
       ++it;
       if (new_seg && !put_q(seg_now, b_now, u_now)) break;
-      y = y2; ks = ks2; ev = ev2;
+      y = y2; ks = ks2; vs = vs2;
     }
     // loads in flight after an abort land before the CTA leaves
     if (lane == 0)

@@ -179,15 +179,13 @@ namespace {
 
 constexpr int PW_THREADS = 256;             // at most: 2 P threads, 4 pieces of 16 dims each, hold a page
 constexpr int PW_MAX_PAGE = 128;
-constexpr int PW_EMIN = -40, PW_EMAX = 60;   // exponents a page scale may have
 
 // The smallest e with amax <= 448 * 2^e (448 = 1.75 * 2^8), held to the range.
 __device__ __forceinline__ int scale_exponent(float amax) {
   const uint32_t u = __float_as_uint(amax);
   const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return min(max(e, PW_EMIN), PW_EMAX);
+  return min(max(e, kScaleExpMin), kScaleExpMax);
 }
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 // The larger absolute values of two pairs of bf16 (a NaN loses), and the same without
 // infinities: a magnitude of 0x7f80 and more is no number.
 __device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t x) {
@@ -308,7 +306,7 @@ __global__ void __launch_bounds__(PW_THREADS, 4) page_write_kernel(
       for (int w = 0; w < threads / 32; ++w) amax = fmaxf(amax, s_max[w]);
       int e = scale_exponent(amax);
       if (o > 0) {
-        const int e_old = scale_exponent(448.f * old_scale);   // the exponent of a stored power of two
+        const int e_old = page_scale_exponent(old_scale);
         e = max(e, e_old);
         if (e > e_old) {
           const float f = pow2(max(e_old - e, -120));

@@ -374,7 +374,9 @@ cslc_status cslc_decode_topk(const float* scores, const int32_t* n_entries, int 
  * values:
  *   codes  [n_pages, H_kv, P, 128] uint8 (e4m3)
  *   scale  [n_pages, H_kv] fp32, a power of two 2^e with -40 <= e <= 60; a
- *          stored value is e4m3(code) * scale (exact in bf16)
+ *          stored value is e4m3(code) * scale (exact in bf16). Only the exponent
+ *          of a scale is read, for keys and for values, held to that range: a
+ *          cache written elsewhere with other scales has to be rescaled first
  * A slot is page * P + offset. Sequence b's token x lies in page
  * block_table[b, x / P] at offset x mod P; an entry of block_table outside
  * [0, n_pages) means that there is no such page. n_pages * P and

@@ -537,6 +537,40 @@ def test_decode_scales_far_apart(C):
     run_decode(C, [700, 129], 8, 2, 16, seed=8, spread=30)
 
 
+def test_scales_are_read_as_their_power_of_two(C):
+    """Of a scale that is no power of two the largest one below it counts, for keys and for values, read and written."""
+    cache, q = make_cache(9, 2, 16, 3), randn((2, 8, 128), 4)
+    table, n = i32([[0, 3, 5, 7], [1, 2, 4, 8]]), i32([60, 33])
+    want = C.page_decode_attn(q, *cache, table, n, SCALE, lse=True)
+    for x in (1.25, 1.9999):
+        for i in (2, 3):
+            odd = list(cache)
+            odd[i] = cache[i] * x
+            got = C.page_decode_attn(q, *odd, table, n, SCALE, lse=True)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), (i, x)
+    kv, slots = randn((3, 2, 128), 5) * 100, i32([16 + 13, 16 + 14, 16 + 15])
+    plain = [x.clone() for x in cache]
+    C.page_write_e4m3(kv, kv, slots, *plain)
+    odd = [x.clone() for x in cache]
+    odd[2], odd[3] = cache[2] * 1.25, cache[3] * 1.9999
+    C.page_write_e4m3(kv, kv, slots, *odd)
+    C.sync_status()
+    assert torch.equal(plain[0], odd[0]) and torch.equal(plain[1], odd[1])
+    assert torch.equal(plain[2][1], odd[2][1]) and torch.equal(plain[3][1], odd[3][1])
+    # out of the range: held to it, in all three
+    far = [x.clone() for x in cache]
+    for x, e in ((0.0, -40), (2.0 ** -41, -40), (2.0 ** 100, 60)):
+        far[2][:], far[3][:] = x, x
+        held = [far[0], far[1], torch.full_like(far[2], 2.0 ** e), torch.full_like(far[3], 2.0 ** e)]
+        for a, b in zip(C.page_decode_attn(q, *far, table, n, SCALE, lse=True), C.page_decode_attn(q, *held, table, n, SCALE, lse=True)):
+            assert torch.equal(a, b), x
+        w = [[y.clone() for y in c] for c in (far, held)]
+        for c in w:
+            C.page_write_e4m3(kv, kv, slots, *c)
+        assert all(torch.equal(a, b) for a, b in zip(w[0][:2], w[1][:2])) and torch.equal(w[0][2][1], w[1][2][1]), x
+    C.sync_status()
+
+
 def test_decode_pages_that_do_not_exist(C):
     run_decode(C, [100, 200, 50], 8, 2, 16, seed=9, bad=[(0, 2, -1), (1, 0, 10 ** 6), (1, 11, -2 ** 31), (2, 0, -1), (2, 1, -1),
                                                          (2, 2, -1), (2, 3, 2 ** 31 - 1)])
