@@ -8,16 +8,19 @@
 //   O^T[dim, head]   = V^T[dim, token] P[token, head]   (M = 128 dims; V MN-major)
 // q and P have 8 significant bits and e4m3 has 4, so each is split into two
 // e4m3 parts that sit side by side as N = 2 GP columns: x = hi + lo / 16, hi =
-// e4m3(x), lo = e4m3(16 (x - hi)). For q (scaled by a power of two to [128,
-// 256) at its largest) the split is exact; for P it is what a rounding to bf16
-// would be (2^-8). Page scales are powers of two: k's multiplies the score, v's
+// e4m3(x), lo = e4m3(16 (x - hi)). From 2^-6 on that is what a rounding to 8
+// significant bits would be (2^-8 of x, exact for a bf16); below, hi is subnormal
+// and x off by at most 2^-14. q is scaled by a power of two to [128, 256) at
+// its row's largest: components from 2^-13 of that one on are exact, smaller ones off
+// by at most 2^-21 of it (a row whose largest is below 2^-110 is scaled less and has
+// fewer bits). Page scales are powers of two: k's multiplies the score, v's
 // is added to the score's exponent before the exponential, so P V needs no
 // scale of its own, and is taken out again (times 2^-e) for the softmax sum.
 // Each tile has its own reference (its exact maximum, mapped to 2^7 .. 2^8): the O^T
 // of a tile is a fresh product, rescaled as it joins the fp32 sum in registers.
-// So a probability is off by at most 2^-21 of the largest one of its own tile,
-// however flat and long the tail is; a running reference would lose tails of
-// 2^-23 per token.
+// So a probability is off by at most 2^-8 of itself and 2^-21 of the largest one of
+// its own tile, however flat and long the tail is; a running reference would lose
+// tails of 2^-23 per token.
 //
 // Work. All tiles of all units, in the order of the sequences, are dealt to the
 // CTAs in equal consecutive ranges (two or three CTAs per SM), whatever the lengths are;
@@ -99,7 +102,7 @@ __device__ __forceinline__ float rcp_approx(float x) {   // within one unit in t
   asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
   return r;
 }
-// Two values as two e4m3 parts each: x = hi + lo / 16, off by at most 2^-8 of x where hi is normal.
+// Two values as two e4m3 parts each: x = hi + lo / 16, off by at most 2^-8 of x where hi is normal, 2^-14 below.
 __device__ __forceinline__ void two_parts(float a, float b, uint32_t& hi, uint32_t& lo) {
   hi = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   const float2 d = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3)));

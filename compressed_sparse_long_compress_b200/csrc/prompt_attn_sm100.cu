@@ -9,11 +9,12 @@
 //
 // CTA roles (persistent, one CTA per SM):
 //   warps 0-3, 4-7  softmax and epilogue of Q tile 0 and 1, thread = row = TMEM
-//                   lane. The row's reference m is the exact maximum of its
+//                   lane. The row's reference is the maximum of its
 //                   first visible tile and moves only when a tile's
 //                   probabilities sum above 2^16 (O in TMEM is rescaled then),
 //                   so the steady state needs no maximum; neither fp32 nor bf16
-//                   loses precision to the larger numbers. P goes back to TMEM
+//                   loses precision to the larger numbers (values have to stay
+//                   below 2^111 over the number of key tiles). P goes back to TMEM
 //                   as bf16 (off by at most 2^-8 of itself) and is the A operand
 //                   of P V from there: no shared memory and no proxy fence.
 //   warp 8          producer: Q tiles (two items), K and V tiles of 64 keys
@@ -72,7 +73,7 @@ constexpr int PA_SLOTS = 6;
 constexpr int PA_Q_BYTES = PA_ROWS * 256;        // two halves of 64 dims
 constexpr int PA_KV_BYTES = PA_KEYS * 256;
 constexpr int PA_KV_HALF = PA_KEYS * 128;
-constexpr float PA_SUM_MAX = 65536.f;            // values of up to 2^111 do not overflow O
+constexpr float PA_SUM_MAX = 65536.f;            // of a tile: values of up to 2^111 / n do not overflow O over n key tiles
 constexpr float PA_FAR = 4194304.f;              // 2^22: up to here m log2(e) scale is off by at most 1/4
 constexpr int PA_SMS = 148;
 constexpr int PA_APART = 450;                    // cycles between the Q tiles' softmaxes, in items of more

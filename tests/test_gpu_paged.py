@@ -19,6 +19,7 @@ import pytest
 import torch
 
 from oracle import paged_oracle as PO
+from oracle.cslc_oracle import e4m3_decode
 from tests.helpers import f64
 
 pytestmark = pytest.mark.gpu
@@ -505,6 +506,27 @@ def test_decode_long_context(C):
 @pytest.mark.parametrize("q_std", [0.0, 0.01, 8.0, 60.0])
 def test_decode_flat_and_peaked(C, q_std):
     run_decode(C, [900, 40], 8, 2, 32, seed=6, q_std=q_std)
+
+
+@pytest.mark.parametrize("wide", [2.0 ** 12, 2.0 ** 16])
+def test_decode_query_with_a_wide_channel(C, wide):
+    """Components of q from 2^-13 of the row's largest on are exact, the others off by at most 2^-21 of it: seen
+    where the keys are 0 in the wide channel."""
+    n, P = 500, 64
+    cache = make_cache(8, 2, P, 31)
+    cache[0][..., 0] = 0
+    q = randn((1, 8, 128), 32)
+    q = torch.sign(q) * (1 + q.abs().clamp(max=0.99)).to(BF16)
+    q[..., 0] = wide
+    table = np.arange(8)[None]
+    out, lse = C.page_decode_attn(q, *cache, i32(table), i32([n]), SCALE, lse=True)
+    C.sync_status()
+    kc, vc, ks, vs = (x.cpu().numpy() for x in cache)
+    ref = list(PO.page_decode_attention(f64(q), kc, vc, ks.astype(float), vs.astype(float), table, [n], SCALE))
+    if wide > 2.0 ** 13:                                       # as if the sum of |q||k| were larger by that error
+        most = np.abs(e4m3_decode(kc) * ks[..., None, None].astype(float)).sum(-1).max()
+        ref[3] = ref[3] + SCALE * 2.0 ** -21 * wide * most / (130 * 2.0 ** -24)
+    check_attention(out, lse, tuple(ref), n)
 
 
 @pytest.mark.parametrize("H,P", [(8, 16), (8, 64), (16, 64)])
