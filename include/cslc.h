@@ -447,6 +447,10 @@ cslc_status cslc_page_write_e4m3(const cslc_bf16* k, const cslc_bf16* v, const i
  * and nk keys, query i sees the keys j <= i + nk - nq). With window > 0 it
  * sees only the last `window` of those.
  *   o[t,h,:] = sum_j softmax_j(scale * q[t,h,:] . k[j,h',:]) v[j,h',:]
+ * It sees the keys that it is passed and no cache: a request that holds tokens
+ * of earlier steps needs their keys and values among k and v. (In a step of
+ * running requests followed by prompts, cu_q = cu_k = cu + (number of running
+ * requests) leaves the running ones' rows to cslc_page_decode_attn.)
  * fp32 statistics and accumulation, probabilities rounded to bf16 for their
  * product with v, bf16 output. A query without a visible key outputs 0 and
  * lse = -inf. Keys and values that a query does not see have no influence on

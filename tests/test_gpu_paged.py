@@ -700,6 +700,43 @@ def test_serving_run(C):
     C.sync_status()
 
 
+@pytest.mark.parametrize("nd,prompts", [(5, [40, 1, 133]), (0, [17]), (3, [])])
+@pytest.mark.parametrize("window", [0, 30])
+def test_step_of_running_requests_and_prompts(C, nd, prompts, window):
+    """One plan and one write for requests of both kinds, running ones first; then each kind's attention into its
+    rows of one output."""
+    P, H, Hkv = 16, 8, 2
+    old = [3, 16, 77, 31, 1][:nd] + [0] * len(prompts)
+    new = [1] * nd + prompts
+    B, n_pages = len(new), 40
+    pages = [-(-n // P) for n in old]
+    pool = np.random.RandomState(nd).permutation(n_pages)
+    table, at = np.full((B, 12), -1), 0
+    for b, m in enumerate(pages):
+        table[b, :m] = pool[at:at + m]
+        at += m
+    cache = make_cache(n_pages, Hkv, P, nd + 1)
+    T = sum(new)
+    q, k, v = randn((T, H, 128), 1), randn((T, Hkv, 128), 2), randn((T, Hkv, 128), 3)
+    table = i32(table)
+    slots, cu, seq_len, status = C.page_plan(i32(old), i32(new), i32(pool[at:]), table, page=P, n_pages=n_pages, max_tokens=T)
+    C.page_write_e4m3(k, v, slots, *cache)
+    out, lse = torch.empty_like(q), torch.empty(T, H, device="cuda")
+    C.page_decode_attn(q[:nd], *cache, table[:nd], seq_len[:nd], SCALE, window, out=out[:nd], lse=lse[:nd])
+    C.prompt_attn(q, k, v, cu[nd:], cu[nd:], SCALE, window, out=out, lse=lse)
+    C.sync_status()
+    assert status.tolist()[1] == 0
+    c = cu.tolist()[nd:]
+    ref = [x.copy() for x in PO.prompt_attention(f64(q), f64(k), f64(v), c, c, SCALE, window)]
+    kc, vc, ks, vs = (x.cpu().numpy() for x in cache)
+    dec = PO.page_decode_attention(f64(q)[:nd], kc, vc, ks.astype(float), vs.astype(float), table.cpu().numpy()[:nd],
+                                   seq_len.tolist()[:nd], SCALE, window)
+    for x, y in zip(ref, dec):
+        x[:nd] = y
+    assert not np.isnan(ref[1]).any()
+    check_attention(out, lse, tuple(ref), 200)
+
+
 def test_calls_on_other_streams_and_repeated(C):
     """Two streams at once, each call twice: the same bits."""
     T, H, Hkv = 700, 8, 2
