@@ -30,10 +30,12 @@
 // (small windows, short tables) of one turn of CTAs go to a CTA each, without that.
 //
 // Measured (64 heads on 8, pages of 128 and 64): 8 requests of up to 131,072 tokens
-// 223 us (6.1 TB/s of codes and scales, 94 % of a copy's rate), 64 of up to 8,192
-// tokens 101 us (81 %): bound by HBM while the CTAs run; the rest is their start,
-// the units' ends and the merge. 16 heads to a key head are bound by the softmax's
-// instructions: 95 us where the bytes take 70.
+// 217-221 us (6.1-6.2 TB/s of codes and scales, 95-97 % of a copy's rate), 64 of up to
+// 8,192 tokens 95-98 us (83-85 %): bound by HBM while the CTAs run; the rest is their
+// start, the units' ends and the merge. 16 heads to a key head are bound by the softmax's
+// instructions: 64 requests of up to 8,192 tokens, 128 heads on 8, 117-121 us where the
+// bytes take 82. Larger groups read the cache once for each 16 heads, every time so
+// bound: 64 heads on one key head 66 us where the bytes take 10.4, 128 on one 113.
 //
 // CTA roles: warps 0-3 softmax (thread = token, then = dim), warp 4 producer
 // (page table and scales, one tile ahead; TMA of each page's codes, STAGES-deep
@@ -114,7 +116,8 @@ __device__ __forceinline__ float pow2i(float d) {
 }
 
 // A softmax warp's mbar_wait, out of line: inlined at each of its waits the code outgrew the instruction
-// cache (16 heads to a key head, pages of 128: 102.8 against 95.1 us; fewer heads: equal).
+// cache (64 requests of up to 8,192 tokens, pages of 128, 128 heads on 8: 130.9 against 118.2 us; 64 heads
+// on 8: equal).
 __device__ __noinline__ bool pd_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int code) {
   return mbar_wait(bar, parity, abort, err, code);
 }
@@ -730,7 +733,7 @@ cslc_status pd_launch(PdShape sh, const uint16_t* q, const uint8_t* k_cache, con
   long long tiles = (tokens + PD_TILE - 1) / PD_TILE;     // of a unit, at most
   if (sh.window > 0 && sh.window < tokens) tiles = min(tiles, ((long long)sh.window + PD_TILE - 2) / PD_TILE + 1);
   // Units that are short at any length of their sequences go whole to a CTA each, which saves the
-  // merge: 30 sequences of 8 key heads, window 512 / 1,024: 18.7 -> 13.2, 22.6 -> 17.7 us. Where
+  // merge: 30 sequences of 8 key heads, window 512 / 1,024: 20.2 -> 14.2, 22.5 -> 17.6 us. Where
   // more of them than CTAs run at a time (64 sequences, window 1,024: 37.5 -> 40.7), or few longer ones
   // (16 units of 9 tiles: 11.4 -> 20.1), the even split is faster.
   sh.whole = units <= most_ctas && (tiles <= 4 || (tiles <= PD_WHOLE && units >= PD_SMS * 7 / 8));

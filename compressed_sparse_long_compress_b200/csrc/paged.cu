@@ -18,9 +18,9 @@
 // a page whose later tokens are larger move its earlier codes to the new
 // scale without a second rounding (but for those that become subnormal).
 // One CTA holds a run in registers between the maximum and the conversion, so
-// the input is read once; HBM bound: 65,536 tokens of 8 heads 70.1 us (5.74 TB/s,
-// 89 % of a copy's rate), 13 prompts of up to 2,001 tokens 20.8 us (16.2 us in a
-// captured graph, 93 %).
+// the input is read once; HBM bound: 65,536 tokens of 8 heads 68.1-69.6 us (5.8-5.9
+// TB/s, 90-91 % of a copy's rate), 13 prompts of up to 2,001 tokens 20.8 us (16.3 us in
+// a captured graph, 92 %).
 
 #include "dependent.cuh"
 

@@ -28,9 +28,9 @@
 // would take 32 (it is bound by reading Q and K), but with 128 keys P has to lie
 // over S, and S of the next tile waits for P V of this one: 16.8 ms against 15.9.
 //
-// Measured (64 heads on 8, causal): 32,768 tokens 15.4 ms = 1,142 TFLOP/s at the
-// power limit (1,665 MHz; cuBLAS sustains 1,387 there), 8,192 tokens 1.01 ms. The
-// tensor-core pipe is busy 78 % of the cycles, the exponential pipe 56 %; without
+// Measured (64 heads on 8, causal): 32,768 tokens 15.3-15.5 ms = 1,135-1,150 TFLOP/s
+// at the power limit (1,665 MHz; cuBLAS sustains 1,387 there), 8,192 tokens 1.01-1.03
+// ms. There the tensor-core pipe is busy 80 % of the cycles, the exponential pipe 61 %; without
 // any softmax arithmetic the same loop reaches 1,228 TFLOP/s. Exponentials moved
 // to the FMA pipe by a polynomial, single instead of packed fp32 operations, and
 // one thread issuing the products were all slower: at the power limit every
