@@ -15,7 +15,9 @@
 // by at most 2^-21 of it (a row whose largest is below 2^-110 is scaled less and has
 // fewer bits). Page scales are powers of two: k's multiplies the score, v's
 // is added to the score's exponent before the exponential, so P V needs no
-// scale of its own, and is taken out again (times 2^-e) for the softmax sum.
+// scale of its own, and is taken out again (times 2^-e) for the softmax sum. Score
+// and exponent are rounded to fp32 as one number: half a step of the score, so that
+// from about 2^16 on equal scores in pages of different V scales weigh apart by that.
 // Each tile has its own reference (its exact maximum, mapped to 2^7 .. 2^8): the O^T
 // of a tile is a fresh product, rescaled as it joins the fp32 sum in registers.
 // So a probability is off by at most 2^-8 of itself and 2^-21 of the largest one of

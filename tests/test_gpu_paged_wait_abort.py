@@ -83,3 +83,27 @@ def test_prompt_waits_that_run_out_at_any_time(C, limit_ns):
     C.sync_status()
     for a, b in zip(got, want):
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("H,limit_ns", [(8, 0), (8, 300), (16, 1000), (8, 4000), (16, 20000)])
+def test_decode_waits_that_run_out_at_any_time(C, H, limit_ns):
+    """As above for the paged decode: units that cross CTAs, pages of 16, and short units of one CTA each."""
+    cache = TP.make_cache(500, 2, 16, 5)
+    table = TP.i32(np.random.RandomState(3).randint(0, 500, (70, 120)))
+    q, n = TP.randn((70, 2 * H, 128), 8), TP.i32(np.random.RandomState(4).randint(0, 1921, 70))
+    run = lambda: [C.page_decode_attn(q, *cache, table, n, TP.SCALE, w, lse=True) for w in (0, 200)]  # noqa: E731
+    want = run()
+    C.sync_status()
+    C.testing_set_wait_limits(limit_ns, 0)
+    for _ in range(10):
+        run()
+        try:
+            C.sync_status()
+        except C.CslcError as e:
+            assert e.status == 7 and "cslc_page_decode_attn" in str(e)
+    C.testing_set_wait_limits(C.WAIT_LIMIT_NS_DEFAULT, C.WAIT_SLEEP_NS_DEFAULT)
+    got = run()
+    C.sync_status()
+    for x, y in zip(got, want):
+        for a, b in zip(x, y):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
